@@ -128,7 +128,8 @@ enum kvq_device_error {
   KVQ_DEVERR_SEQ_LEN = 2u,     /* seq_lens[b] > max_seq_len or capacity (clamped)     */
   KVQ_DEVERR_TIMEOUT = 4u,     /* a bounded shared-memory pipeline wait gave up       */
   KVQ_DEVERR_BAD_POS = 8u,     /* pos[b] < 0 (rows skipped)                            */
-  KVQ_DEVERR_BAD_PAGE = 16u    /* block_table entry outside [0, num_pages) (see below) */
+  KVQ_DEVERR_BAD_PAGE = 16u,   /* block_table entry outside [0, num_pages) (see below) */
+  KVQ_DEVERR_NO_PAGE = 32u     /* kvq_plan_append: no free page, or the row's last page is shared */
 };
 
 /* Bits of kvq_cache_desc.flags. */
@@ -378,6 +379,154 @@ int kvq_decode_attention_static(const kvq_cache_desc* cache, const void* q,
  */
 int32_t kvq_decode_split_tokens(const kvq_cache_desc* cache,
                                 int32_t num_q_heads, int32_t max_seq_len);
+
+/* ------------------------------------------------------------------------
+ * A serving step over a ragged batch: rows that bring different numbers of
+ * new tokens (prefill chunks, draft tokens to verify, single tokens, none).
+ * The tokens of all rows are packed one after another, [num_tokens][heads][D],
+ * row b's at [cu_tokens[b], cu_tokens[b + 1]).  Per step kvq_plan_append()
+ * once, then per layer kvq_quantize_append_ragged() and
+ * kvq_chunk_attention().  (The summary page describes no serving system;
+ * these calls write and read the cache format above, unchanged.)
+ *
+ * The slot map says where the packed tokens go.  Entry e is four int32:
+ *   slot_map[4e + 0]  block: a page of the pool (paged layout) or a batch row
+ *   slot_map[4e + 1]  local position in the block of the entry's first token
+ *   slot_map[4e + 2]  index of that token among the packed ones
+ *   slot_map[4e + 3]  count: 1 .. 16 tokens at consecutive positions of one
+ *                     16-position tile; 0: the entry is not used
+ */
+
+/*
+ * Entries of a slot map for `num_tokens` packed tokens in `batch` rows, at
+ * most: min(num_tokens, num_tokens / 16 + 2 * batch).  0 if an argument is
+ * negative.  Pure host function.
+ */
+int32_t kvq_slot_map_entries(int32_t batch, int32_t num_tokens);
+
+/*
+ * Plans the step: from every row's length before and after it, the pages the
+ * rows need are taken from the pool (or returned to it, when a row gets
+ * shorter: rejected draft tokens; length 0: a finished request), the block
+ * table is updated, and the offsets and the slot map of the packed tokens
+ * are written.  One kernel launch.
+ *
+ *   old_lens, new_lens : device int32[B], 0 .. capacity.
+ *   num_tokens : tokens in the packed tensors, >= sum of max(0, new - old).
+ *   page_users : paged layout: device int32[num_pages], the number of block
+ *                table entries that name each page (0: free); updated.  Rows
+ *                that share prefix pages count once each.  NULL without
+ *                pages.
+ *   lens       : device int32[B], written: the rows' lengths after the call.
+ *   cu_tokens  : device int32[B + 1], written: cu_tokens[0] = 0,
+ *                cu_tokens[b + 1] = cu_tokens[b] + max(0, new_lens[b] - old_lens[b]).
+ *   slot_map   : device int32[num_entries][4], 16-byte aligned, written;
+ *                num_entries >= kvq_slot_map_entries(B, num_tokens).  Entries
+ *                in row order, positions ascending; the unused last ones are
+ *                zero.  May be NULL when num_entries is 0.
+ *
+ * cache->block_table is read and written (entries [ceil(old/P), ceil(new/P))
+ * of a growing row; those of a shrinking row become -1).  Returned pages are
+ * free again within the call.  Free pages are given out in ascending order
+ * to the rows in order, so the result does not depend on timing.
+ * A row is refused - lens[b] = old_lens[b], no page taken, none of its
+ * tokens in the map, its place in cu_tokens kept - when no page is left for
+ * it (this and later rows that need pages), or when it would write into a
+ * partly filled last page that other rows share (both KVQ_DEVERR_NO_PAGE:
+ * give the row a copy of that page first), or when that page's entry is
+ * outside the pool (KVQ_DEVERR_BAD_PAGE).  A row with a length below 0
+ * (KVQ_DEVERR_BAD_POS) or above capacity (KVQ_DEVERR_SEQ_LEN) is refused and
+ * counts no tokens.  More tokens than num_tokens flag KVQ_DEVERR_CAPACITY;
+ * those past it are in no entry.
+ * batch <= 8192 (KVQ_ERR_UNSUPPORTED above).  Calls that update the same
+ * table or pool must be ordered by their streams.
+ */
+int kvq_plan_append(const kvq_cache_desc* cache, const int32_t* old_lens,
+                    const int32_t* new_lens, int32_t num_tokens, int32_t* page_users,
+                    int32_t* lens, int32_t* cu_tokens, int32_t* slot_map,
+                    int32_t num_entries, kvq_stream_t stream);
+
+/*
+ * Quantizes packed tokens into the places of a slot map: the same quantizer
+ * and format, bit for bit, as kvq_quantize_append().
+ *
+ *   k, v     : device, token t of kv head h at element offset
+ *              t * stride + h * D, in_dtype, 16-byte aligned.
+ *   k_stride, v_stride : elements from one token to the next, >= Hkv * D and
+ *              a multiple of 16 bytes (Hkv * D when packed; more when k and v
+ *              are slices of one projection's output).
+ *   slot_map : device int32[num_entries][4], 16-byte aligned, as written by
+ *              kvq_plan_append().  No position may be named twice.
+ * Entries whose block is outside the cache flag KVQ_DEVERR_BAD_PAGE, whose
+ * positions leave the block or one tile KVQ_DEVERR_CAPACITY, whose tokens
+ * are outside [0, num_tokens) KVQ_DEVERR_BAD_POS; they are skipped.
+ * Positions of no entry keep their bytes.  One kernel launch.
+ */
+int kvq_quantize_append_ragged(const kvq_cache_desc* cache, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, int32_t in_dtype,
+                               int32_t num_tokens, const int32_t* slot_map,
+                               int32_t num_entries, kvq_stream_t stream);
+
+/*
+ * The reverse: the values that the cache holds at the places of a slot map,
+ * code * scale + zero in binary32, rounded once to out_dtype.  Keys of a
+ * rotated cache come back in their own basis, H k^ / D.  (To re-encode a
+ * prefix at other widths, to move rows to another cache, to inspect.)
+ *
+ *   k_out, v_out : device, [num_tokens][Hkv][D] packed, 16-byte aligned.
+ *                  Tokens that no entry names are left as they were.
+ * Entries are checked as in kvq_quantize_append_ragged().  One kernel launch.
+ */
+int kvq_dequantize_ragged(const kvq_cache_desc* cache, const int32_t* slot_map,
+                          int32_t num_entries, void* k_out, void* v_out, int32_t out_dtype,
+                          int32_t num_tokens, kvq_stream_t stream);
+
+/*
+ * Workspace bytes kvq_chunk_attention() needs for these arguments on the
+ * current device, whatever its element types; 0 if they are invalid or none
+ * is needed.
+ */
+size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_heads,
+                                 int32_t num_tokens, int32_t max_q_len, int32_t max_seq_len);
+
+/*
+ * Attention of every row's new tokens over the packed cache, which holds
+ * them already:
+ *   s_t = sm_scale * sum_d q_d * k^_{t,d},   o_d = sum_t softmax(s)_t * v^_{t,d}
+ * where query i of the n_b queries of row b attends to the positions
+ *   t in [0, seq_lens[b] - n_b + i]  (causal != 0), or [0, seq_lens[b]).
+ * A query that sees no position yields o = 0.
+ *
+ *   q           : device, token t of query head hq at t * q_stride + hq * D,
+ *                 q_dtype, 16-byte aligned; q_stride >= Hq * D, a multiple of
+ *                 16 bytes.
+ *   num_q_heads : Hq, a multiple of Hkv (head hq reads kv head hq / (Hq / Hkv)).
+ *   num_tokens  : packed tokens of q and out.
+ *   cu_tokens   : device int32[B + 1], ascending from 0; row b's tokens are
+ *                 [cu_tokens[b], cu_tokens[b + 1]).  Tokens from
+ *                 cu_tokens[B] on are left as they were in out.
+ *   seq_lens    : device int32[B]: cached positions of each row, its new
+ *                 tokens among them.
+ *   max_q_len   : host upper bound of every row's n_b; when it is 1 and
+ *                 num_tokens = B, every row has to have its one token.
+ *   max_seq_len : host upper bound of seq_lens.
+ *   sm_scale    : softmax scale; <= 0 selects 1/sqrt(D).
+ *   out         : device, [num_tokens][Hq][D] packed, out_dtype, 16-byte aligned.
+ *   workspace   : kvq_chunk_workspace_bytes(), 16-byte aligned; it may be
+ *                 shared by calls that are ordered by their streams.
+ *
+ * Lengths above max_seq_len or capacity are clamped and flag
+ * KVQ_DEVERR_SEQ_LEN; rows whose offsets are not ascending, pass num_tokens
+ * or exceed max_q_len are skipped and flag KVQ_DEVERR_BAD_POS.  Block-table
+ * entries outside the pool flag KVQ_DEVERR_BAD_PAGE, are not followed, and
+ * leave that row's output unspecified.
+ */
+int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_stride,
+                        int32_t q_dtype, int32_t num_q_heads, int32_t num_tokens,
+                        const int32_t* cu_tokens, const int32_t* seq_lens, int32_t max_q_len,
+                        int32_t max_seq_len, int32_t causal, float sm_scale, void* out,
+                        int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                        kvq_stream_t stream);
 
 /*
  * Failure-detection test knob; not for production use.  The summary page has

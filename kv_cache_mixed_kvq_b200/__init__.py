@@ -15,6 +15,14 @@ Typical use::
     # or both in one launch, the new rows at seq_lens - n .. seq_lens - 1:
     out = kvq_append_decode_attention(cache, k, v, q, seq_lens, max_seq_len)
 
+A serving step whose rows bring different numbers of new tokens (prefill
+chunks, draft tokens, single tokens), packed one after another::
+
+    lens, cu, slots = kvq_plan_append(cache, old_lens, new_lens, k.shape[0], page_users)
+    # then, for every layer:
+    kvq_quantize_append_ragged(cache, k, v, slots)                # k, v: [T][Hkv][D]
+    out = kvq_chunk_attention(cache, q, cu, lens, max_q, max_len)  # q: [T][Hq][D]
+
 A paged cache (block tables) is allocated with ``page_size``, ``num_pages``
 and an int32 ``block_table`` [batch][capacity / page_size].
 """
@@ -33,7 +41,7 @@ LIBRARY_PATH = os.path.join(_HERE, "libkvq.so")
 KVQ_F32, KVQ_BF16, KVQ_F16 = 0, 1, 2
 KVQ_OK, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA = range(5)
 KVQ_DEVERR_CAPACITY, KVQ_DEVERR_SEQ_LEN, KVQ_DEVERR_TIMEOUT, KVQ_DEVERR_BAD_POS = 1, 2, 4, 8
-KVQ_DEVERR_BAD_PAGE = 16
+KVQ_DEVERR_BAD_PAGE, KVQ_DEVERR_NO_PAGE = 16, 32
 KVQ_K_CODES, KVQ_V_CODES, KVQ_K_PARAMS, KVQ_V_PARAMS = range(4)
 KVQ_FLAG_ROTATE_KEYS, KVQ_FLAG_PAGED = 1, 2
 
@@ -89,6 +97,20 @@ def library() -> ctypes.CDLL:
     lib.kvq_append_decode_attention.argtypes = [D, P, P, I32, I32, P, I32, I32, P, I32,
                                                 ctypes.c_float, P, I32, P, SZ, P]
     lib.kvq_append_decode_attention.restype = ctypes.c_int
+    I64 = ctypes.c_int64
+    lib.kvq_slot_map_entries.argtypes = [I32, I32]
+    lib.kvq_slot_map_entries.restype = I32
+    lib.kvq_plan_append.argtypes = [D, P, P, I32, P, P, P, P, I32, P]
+    lib.kvq_plan_append.restype = ctypes.c_int
+    lib.kvq_quantize_append_ragged.argtypes = [D, P, I64, P, I64, I32, I32, P, I32, P]
+    lib.kvq_quantize_append_ragged.restype = ctypes.c_int
+    lib.kvq_dequantize_ragged.argtypes = [D, P, I32, P, P, I32, I32, P]
+    lib.kvq_dequantize_ragged.restype = ctypes.c_int
+    lib.kvq_chunk_workspace_bytes.argtypes = [D, I32, I32, I32, I32]
+    lib.kvq_chunk_workspace_bytes.restype = SZ
+    lib.kvq_chunk_attention.argtypes = [D, P, I64, I32, I32, I32, P, P, I32, I32, I32,
+                                        ctypes.c_float, P, I32, P, SZ, P]
+    lib.kvq_chunk_attention.restype = ctypes.c_int
     lib.kvq_device_error_flags.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     lib.kvq_device_error_flags.restype = ctypes.c_int
     lib.kvq_last_device_error.argtypes = [P]
@@ -276,6 +298,183 @@ def kvq_append_decode_attention(cache: KVCache, k_new: torch.Tensor, v_new: torc
         _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len), float(sm_scale), _dev_ptr(out, "out"),
         _DTYPE[out.dtype], ws_ptr, ws_bytes, _stream_ptr(stream))
     _check(st, "kvq_append_decode_attention")
+    return out
+
+
+# ------------------------------------------- a serving step over a ragged batch
+def _on_current(device: torch.device) -> None:
+    """The library launches on the current device: its tensors must be there."""
+    if device.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _int32(t: torch.Tensor, numel: int, name: str, device: torch.device) -> int:
+    """Data pointer of a contiguous int32 tensor of `numel` elements."""
+    if t.dtype != torch.int32 or t.numel() != numel:
+        raise ValueError(f"{name} must be an int32 tensor of {numel} elements")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the cache's device")
+    return _dev_ptr(t, name)
+
+
+def _tokens(t: torch.Tensor, heads: Optional[int], D: int, name: str, device: torch.device):
+    """(data pointer, elements from token to token) of packed tokens [T][heads][D];
+    a slice along the heads of a larger packed tensor is accepted."""
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens][{heads or 'heads'}][{D}]")
+    if t.dtype not in _DTYPE:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the cache's device")
+    T, H, _ = t.shape
+    if T == 0:
+        return None, H * D
+    stride = t.stride(0) if T > 1 else H * D
+    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and H > 1) or stride < H * D or \
+            stride * t.element_size() % 16:
+        raise ValueError(f"{name}: the heads of a token must be contiguous and tokens "
+                         "a multiple of 16 bytes apart")
+    return t.data_ptr(), stride
+
+
+def _slots(slot_map: torch.Tensor, device: torch.device):
+    if slot_map.dim() != 2 or slot_map.shape[1] != 4:
+        raise ValueError("slot_map must be [entries][4]")
+    return _int32(slot_map, slot_map.numel(), "slot_map", device)
+
+
+def kvq_slot_map_entries(batch: int, num_tokens: int) -> int:
+    """Entries of a slot map for num_tokens packed tokens in batch rows, at most."""
+    return int(library().kvq_slot_map_entries(batch, num_tokens))
+
+
+def kvq_plan_append(cache: KVCache, old_lens: torch.Tensor, new_lens: torch.Tensor,
+                    num_tokens: int, page_users: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """Plan one ragged step: (lens, cu_tokens, slot_map) for rows that go from
+    old_lens to new_lens with num_tokens new tokens in all (or more).
+
+    A paged cache's block_table and page_users (int32 [num_pages], users of
+    each page) are updated in place: growing rows take free pages, shrinking
+    rows return theirs.  A row that gets no page keeps its old length in lens
+    and flags KVQ_DEVERR_NO_PAGE."""
+    device = cache.k_codes.device
+    _on_current(device)
+    B = cache.batch
+    old, new = _int32(old_lens, B, "old_lens", device), _int32(new_lens, B, "new_lens", device)
+    if cache.page_size:
+        if page_users is None:
+            raise ValueError("a paged cache needs page_users")
+        users = _int32(page_users, cache.num_pages, "page_users", device)
+    else:
+        if page_users is not None:
+            raise ValueError("page_users is for paged caches")
+        users = None
+    lib = library()
+    E = lib.kvq_slot_map_entries(B, num_tokens)
+    slot_map = torch.empty((E, 4), dtype=torch.int32, device=device)
+    lens = torch.empty(B, dtype=torch.int32, device=device)
+    cu = torch.empty(B + 1, dtype=torch.int32, device=device)
+    d = cache.desc()
+    st = lib.kvq_plan_append(ctypes.byref(d), old, new, num_tokens, users, lens.data_ptr(),
+                             cu.data_ptr(), slot_map.data_ptr() if E else None, E,
+                             _stream_ptr(stream))
+    _check(st, "kvq_plan_append")
+    return lens, cu, slot_map
+
+
+def kvq_quantize_append_ragged(cache: KVCache, k: torch.Tensor, v: torch.Tensor,
+                               slot_map: torch.Tensor,
+                               stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantize packed tokens k, v ([T][Hkv][D]) into the places of a slot map."""
+    device = cache.k_codes.device
+    _on_current(device)
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must be tensors of one shape and dtype")
+    kp, ks = _tokens(k, cache.kv_heads, cache.head_dim, "k", device)
+    vp, vs = _tokens(v, cache.kv_heads, cache.head_dim, "v", device)
+    sp = _slots(slot_map, device)
+    d = cache.desc()
+    st = library().kvq_quantize_append_ragged(ctypes.byref(d), kp, ks, vp, vs, _DTYPE[k.dtype],
+                                              k.shape[0], sp, slot_map.shape[0],
+                                              _stream_ptr(stream))
+    _check(st, "kvq_quantize_append_ragged")
+
+
+def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: int,
+                          dtype: torch.dtype = torch.bfloat16,
+                          k_out: Optional[torch.Tensor] = None,
+                          v_out: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None):
+    """(k, v) [num_tokens][Hkv][D] that the cache holds at the places of a slot
+    map, as dtype (or into k_out, v_out, contiguous and of one dtype).  Tokens
+    that no entry names are not written."""
+    device = cache.k_codes.device
+    _on_current(device)
+    shape = (num_tokens, cache.kv_heads, cache.head_dim)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both of k_out and v_out, or neither")
+    if k_out is None:
+        if dtype not in _DTYPE:
+            raise ValueError("dtype must be float32, bfloat16 or float16")
+        k_out = torch.empty(shape, dtype=dtype, device=device)
+        v_out = torch.empty(shape, dtype=dtype, device=device)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if tuple(t.shape) != shape or t.dtype not in _DTYPE or t.dtype != k_out.dtype or \
+                t.device != device:
+            raise ValueError(f"{name} must be {list(shape)}, on the cache's device, of one dtype")
+    sp = _slots(slot_map, device)
+    d = cache.desc()
+    st = library().kvq_dequantize_ragged(ctypes.byref(d), sp, slot_map.shape[0],
+                                         _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"),
+                                         _DTYPE[k_out.dtype], num_tokens, _stream_ptr(stream))
+    _check(st, "kvq_dequantize_ragged")
+    return k_out, v_out
+
+
+def kvq_chunk_workspace_bytes(cache: KVCache, num_q_heads: int, num_tokens: int, max_q_len: int,
+                              max_seq_len: int) -> int:
+    d = cache.desc()
+    return int(library().kvq_chunk_workspace_bytes(ctypes.byref(d), num_q_heads, num_tokens,
+                                                   max_q_len, max_seq_len))
+
+
+def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor,
+                        seq_lens: torch.Tensor, max_q_len: int, max_seq_len: int,
+                        causal: bool = True, sm_scale: float = 0.0,
+                        out: Optional[torch.Tensor] = None,
+                        out_dtype: Optional[torch.dtype] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of packed queries q ([T][Hq][D]) over the cache, which holds
+    their tokens already: query i of row b's n_b = cu_tokens[b+1] - cu_tokens[b]
+    attends to positions [0, seq_lens[b] - n_b + i] (causal) or [0, seq_lens[b])."""
+    device = cache.k_codes.device
+    _on_current(device)
+    qp, qs = _tokens(q, None, cache.head_dim, "q", device)
+    T, Hq, D = q.shape
+    cu = _int32(cu_tokens, cache.batch + 1, "cu_tokens", device)
+    lens = _int32(seq_lens, cache.batch, "seq_lens", device)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=device)
+    elif out.shape != q.shape or out.dtype not in _DTYPE or out.device != device:
+        raise ValueError("out must be of q's shape, on the cache's device")
+    d = cache.desc()
+    lib = library()
+    if workspace is None:  # (a given workspace is checked by the library itself)
+        need = lib.kvq_chunk_workspace_bytes(ctypes.byref(d), Hq, T, max_q_len, max_seq_len)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    ws_ptr = _dev_ptr(workspace, "workspace") if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib.kvq_chunk_attention(ctypes.byref(d), qp, qs, _DTYPE[q.dtype], Hq, T, cu, lens,
+                                 max_q_len, max_seq_len, 1 if causal else 0, sm_scale,
+                                 _dev_ptr(out, "out"), _DTYPE[out.dtype], ws_ptr, ws_bytes,
+                                 _stream_ptr(stream))
+    _check(st, "kvq_chunk_attention")
     return out
 
 

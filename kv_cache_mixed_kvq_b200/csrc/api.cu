@@ -12,6 +12,7 @@
 #include <tuple>
 #include <utility>
 
+#include "host.h"
 #include "internal.h"
 
 namespace kvq {
@@ -70,9 +71,7 @@ static __device__ uint32_t g_kvq_device_error;
 static std::atomic<long long> g_fault_stage{-1};
 static std::atomic<long long> g_fault_limit_ns{0};
 
-namespace {
-
-using kvq::DecodeKernel;
+namespace kvq {
 
 constexpr int kMaxDevices = 64;
 
@@ -156,6 +155,12 @@ int error_word(uint32_t** out) {
   *out = ptrs[dev];
   return KVQ_OK;
 }
+
+}  // namespace kvq
+
+namespace {
+
+using namespace kvq;
 
 int variant_of(int heads_per_cta, int q_dtype);
 

@@ -1,0 +1,76 @@
+// Kernel launches of a ragged serving step: planning, append, read-back and
+// chunk attention (declared for the host entry points in api_serve.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvq.h"
+
+namespace kvq {
+
+// Rows one planning call takes (their prefix sums live in shared memory).
+constexpr int kPlanRows = 8192;
+
+struct PlanArgs {
+  const int32_t* old_lens;
+  const int32_t* new_lens;
+  int batch, capacity, num_tokens, num_entries;
+  int32_t* users;  // pages' user counts (NULL: slot layout)
+  int32_t* table;  // block table (NULL: slot layout)
+  int page_shift, pages_per_seq, num_pages;
+  int32_t* lens;
+  int32_t* cu;
+  int4* map;
+  uint32_t* err;
+};
+
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream);
+
+// One layer's packed cache as a number of equal blocks: the pages of the
+// pool, or the batch rows' slots.
+struct BlockCache {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint32_t* k_params;
+  uint32_t* v_params;
+  int kv_heads, head_dim, bits_k, bits_v, group, group_v;
+  int blocks;        // pages, or batch rows
+  int block_tokens;  // positions of a block
+  bool rotate_keys;
+};
+
+struct RaggedArgs {
+  BlockCache c;
+  const void* k;  // append: inputs; read-back: outputs (written through)
+  const void* v;
+  int64_t k_stride, v_stride;  // elements from one token to the next
+  int dtype, num_tokens, num_entries;
+  const int4* map;
+  uint32_t* err;
+};
+
+cudaError_t launch_append_ragged(const RaggedArgs& a, cudaStream_t stream);
+cudaError_t launch_dequantize_ragged(const RaggedArgs& a, cudaStream_t stream);
+
+struct ChunkArgs {
+  BlockCache c;
+  const int32_t* table;  // block table (NULL: slot layout)
+  int page_shift, pages_per_seq;
+  int batch, capacity;
+  const void* q;
+  int64_t q_stride;
+  int q_dtype, q_heads, gq, num_tokens;
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  int max_q_len, max_seq_len;
+  bool causal;
+  float sm_scale_log2;  // softmax scale times log2(e)
+  void* out;
+  int out_dtype;
+  uint32_t* err;
+};
+
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream);
+
+}  // namespace kvq
