@@ -87,7 +87,6 @@ int check_shape(int B, int Hkv, int D, int cap, int bk, int bv, int G) {
   if (!valid_bits(bk) || !valid_bits(bv)) return KVQ_ERR_UNSUPPORTED;
   if (G != 32 && G != 64 && G != 128) return KVQ_ERR_UNSUPPORTED;
   if (G > D) return KVQ_ERR_INVALID_ARG;
-  if (B > 65535 || Hkv > 65535) return KVQ_ERR_UNSUPPORTED;  // grid limits
   return KVQ_OK;
 }
 
@@ -100,6 +99,8 @@ int check_cache(const kvq_cache_desc* c) {
   int st = check_shape(c->batch, c->kv_heads, c->head_dim, c->capacity, c->bits_k, c->bits_v,
                        c->group);
   if (st != KVQ_OK) return st;
+  // grid limits (of the batch rows; a pool may have any number of pages)
+  if (c->batch > 65535 || c->kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
   const int gv = group_v_of(c);
   st = check_shape(c->batch, c->kv_heads, c->head_dim, c->capacity, c->bits_k, c->bits_v, gv);
   if (st != KVQ_OK) return st;

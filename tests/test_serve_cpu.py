@@ -138,3 +138,12 @@ def test_python_calls_want_cuda_tensors():
                  lambda: kvq.kvq_chunk_attention(cache, x, i3, i2, 4, 64)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_pools_of_many_pages():
+    """The number of pages is not bound by a grid's limits (batch rows are)."""
+    page = kvq.kvq_cache_bytes(1, 2, 128, 32, 4, 2, 64, kvq.KVQ_K_CODES)
+    assert kvq.kvq_cache_bytes(200000, 2, 128, 32, 4, 2, 64, kvq.KVQ_K_CODES) == 200000 * page
+    lib = kvq.library()
+    assert lib.kvq_validate_cache(ctypes.byref(_desc(**dict(PAGED, num_pages=200000)))) == OK
+    assert lib.kvq_validate_cache(ctypes.byref(_desc(batch=65536))) == UNSUP
