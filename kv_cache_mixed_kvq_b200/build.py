@@ -1,13 +1,14 @@
 """Build libkvq.so in-tree for B200 (sm_100a) with nvcc.
 
 Each CUDA source is compiled to an object under _build/ (in parallel, and
-only when it or a header changed), then linked into
+only when it or a header that it includes changed), then linked into
 kv_cache_mixed_kvq_b200/libkvq.so.  Usage: python -m kv_cache_mixed_kvq_b200.build
 """
 from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -26,14 +27,24 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "-I", INCLUDE, "-I", CSRC]
 
 
-def _headers():
-    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+def _with_headers(src: str) -> set:
+    """src and every header of this repository that it includes."""
+    seen, todo = set(), [src]
+    while todo:
+        path = todo.pop()
+        if path in seen:
+            continue
+        seen.add(path)
+        with open(path) as f:
+            names = re.findall(r'^#include "([^"]+)"', f.read(), re.M)
+        todo += [p for n in names for p in (os.path.join(CSRC, n), os.path.join(INCLUDE, n))
+                 if os.path.exists(p)]
+    return seen
 
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    newest = max(os.path.getmtime(p) for p in [src] + _headers())
+    newest = max(os.path.getmtime(p) for p in _with_headers(src))
     if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
         return obj
     cmd = [NVCC] + ARCH + FLAGS + ["-c", src, "-o", obj + ".tmp"]

@@ -69,9 +69,65 @@ int check_chunk(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len, 
   if (st != KVQ_OK) return st;
   if (Hq < 1 || Hq % c->kv_heads != 0 || num_tokens < 0 || max_q_len < 0 || max_seq_len < 0)
     return KVQ_ERR_INVALID_ARG;
+  if (c->batch > kChunkRows) return KVQ_ERR_UNSUPPORTED;
   // the (token, query head) rows are counted in 32 bits
   if (static_cast<long long>(num_tokens) * Hq > 0x7fffffffll / 2) return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;
+}
+
+// Binary16 pieces of the operands (see chunk.cuh).  A rotated binary16 query
+// is a sum, no longer exact in one piece.
+int pieces_of(const kvq_cache_desc* c, int q_dtype) {
+  if (q_dtype == KVQ_BF16) return 1;
+  return q_dtype == KVQ_F32 || (c->flags & KVQ_FLAG_ROTATE_KEYS) ? 3 : 2;
+}
+
+struct ChunkPlan {
+  int grid, max_units, part_rows;
+  bool whole_units;
+  size_t ml_offset, o_offset, bytes;  // workspace: headers, (m, l), o
+};
+
+// Fewest steps of a CTA's share: below it the set-up of a CTA and the joining
+// of its partial results cost more than the steps.
+constexpr int kMinShare = 2;
+
+// Division of work, from the host's bounds alone (the lengths are on the
+// device): one CTA per SM, fewer when there cannot be that much work.  Units
+// of at most kMinShare steps stay whole, which saves the joining launch.
+int chunk_plan(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len, int max_seq_len,
+               int pieces, ChunkPlan* p) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  const int gq = Hq / c->kv_heads, unit = unit_rows(pieces);
+  const int q_len = std::min(max_q_len, num_tokens);
+  const long long rows = static_cast<long long>(q_len) * gq;
+  const long long units =
+      (static_cast<long long>(num_tokens) * gq / unit + std::min(c->batch, num_tokens)) *
+      c->kv_heads;
+  const int len = std::min(max_seq_len, c->capacity);
+  const int tile = tile_tokens(pieces, c->head_dim, c->bits_k + c->bits_v);
+  const long long tiles = (len + tile - 1) / tile;
+  const long long steps = std::max(1ll, rows > 128 && unit > 128 ? tiles : (tiles + 1) / 2);
+  p->whole_units = steps <= kMinShare;
+  p->max_units = static_cast<int>((rows + unit - 1) / unit);
+  p->grid = static_cast<int>(std::min<long long>(
+      sms, p->whole_units ? units : (units * steps + kMinShare - 1) / kMinShare));
+  p->grid = std::max(1, p->grid);
+  p->part_rows = static_cast<int>(std::min<long long>(unit, std::max(1ll, rows)));
+  const size_t places = static_cast<size_t>(p->grid) * 2;
+  p->ml_offset = places * 32;
+  p->o_offset = (p->ml_offset + places * p->part_rows * 8 + 15) / 16 * 16;
+  p->bytes = p->whole_units ? 0 : p->o_offset + places * p->part_rows * c->head_dim * 4;
+  return KVQ_OK;
+}
+
+// One token in every batch row, of a 16-bit type: the decode kernel's case
+// (max_q_len and num_tokens leave nothing else).
+bool is_decode(const kvq_cache_desc* c, int num_tokens, int max_q_len) {
+  return max_q_len == 1 && num_tokens == c->batch;
 }
 
 }  // namespace
@@ -137,7 +193,16 @@ int kvq_dequantize_ragged(const kvq_cache_desc* cache, const int32_t* slot_map,
 size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_heads,
                                  int32_t num_tokens, int32_t max_q_len, int32_t max_seq_len) {
   if (check_chunk(cache, num_q_heads, num_tokens, max_q_len, max_seq_len) != KVQ_OK) return 0;
-  return 0;
+  size_t need = 0;
+  for (int pieces = 1; pieces <= 3; ++pieces) {
+    ChunkPlan p;
+    if (chunk_plan(cache, num_q_heads, num_tokens, max_q_len, max_seq_len, pieces, &p) != KVQ_OK)
+      return 0;
+    need = std::max(need, p.bytes);
+  }
+  if (is_decode(cache, num_tokens, max_q_len))
+    need = std::max(need, kvq_decode_workspace_bytes(cache, num_q_heads, max_seq_len));
+  return need;
 }
 
 int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_stride,
@@ -155,6 +220,16 @@ int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_st
       !aligned(cu_tokens, 4) || !aligned(seq_lens, 4) ||
       !valid_stride(q_stride, num_q_heads, cache->head_dim, q_dtype))
     return KVQ_ERR_INVALID_ARG;
+  if (is_decode(cache, num_tokens, max_q_len) && q_dtype != KVQ_F32 &&
+      q_stride == static_cast<int64_t>(num_q_heads) * cache->head_dim)
+    return kvq_decode_attention(cache, q, q_dtype, num_q_heads, seq_lens, max_seq_len, sm_scale,
+                                out, out_dtype, workspace, workspace_bytes, stream);
+  const int pieces = pieces_of(cache, q_dtype);
+  ChunkPlan p;
+  st = chunk_plan(cache, num_q_heads, num_tokens, max_q_len, max_seq_len, pieces, &p);
+  if (st != KVQ_OK) return st;
+  if (p.bytes > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes))
+    return KVQ_ERR_WORKSPACE;
   const float scale =
       sm_scale > 0.0f ? sm_scale : 1.0f / sqrtf(static_cast<float>(cache->head_dim));
   ChunkArgs a;
@@ -177,9 +252,17 @@ int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_st
   a.sm_scale_log2 = scale * 1.4426950408889634f;
   a.out = out;
   a.out_dtype = out_dtype;
+  a.whole_units = p.whole_units;
+  a.min_share = p.whole_units ? 1 : kMinShare;
+  a.max_units = p.max_units;
+  a.part_rows = p.part_rows;
+  uint8_t* ws = p.bytes > 0 ? static_cast<uint8_t*>(workspace) : nullptr;
+  a.ws_head = reinterpret_cast<int*>(ws);
+  a.ws_ml = reinterpret_cast<float2*>(ws ? ws + p.ml_offset : nullptr);
+  a.ws_o = reinterpret_cast<float*>(ws ? ws + p.o_offset : nullptr);
   st = error_word(&a.err);
   if (st != KVQ_OK) return st;
-  return to_status(launch_chunk(a, reinterpret_cast<cudaStream_t>(stream)));
+  return to_status(launch_chunk(a, pieces, p.grid, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,1239 @@
+// Attention of a chunk of new tokens over the packed cache
+// (kvq_chunk_attention), on the Blackwell tensor cores.
+//
+//   s_it = scale q_i . k^_t,  p_it = exp(s_it - m_i),  o_i = sum_t p_it v^_t / sum_t p_it
+// in one pass over the positions t with a running reference m_i of the
+// exponents: m_i follows the running maximum, but o_i and l_i = sum_t p_it are
+// rescaled (by exp(m_i - m_i')) only when the maximum has grown by more than a
+// factor 2^kThreshold, since any reference cancels in the quotient.  The query
+// heads of one kv head share its keys, so a row of a tile is a (token, head)
+// pair: row r of batch row b is its new token r / gq, head r mod gq of the kv
+// head.
+//
+// Products: S = Q K^T and O += P V by tcgen05.mma (kind::f16, binary32
+// accumulators in tensor memory), 128 rows x NT positions x D.  Operands are
+// binary16, keys and values unpacked to it in the kernel.  How many binary16
+// pieces hold an operand follows from the query's type (PIECES):
+//   1  bf16: a query row, scaled by a power of two, is exact in binary16; keys,
+//      values and weights are rounded once, 2^-11, an eighth of the output's
+//      2^-8;
+//   2  f16: query exact, keys and values in two pieces (hi + lo, 2^-22): a
+//      score's error is the keys' relative error times the sum of magnitudes,
+//      which one piece would make several times the output's 2^-11;
+//   3  f32: query, keys, weights and values in two pieces, products hi hi +
+//      hi lo + lo hi, 2^-22 in all.
+// Softmax statistics, sums and outputs are binary32.
+//
+// Roles (20 warps, one CTA per SM):
+//   warps 0-7   softmax: two slots of four warps; one thread a row of its slot
+//   warps 8-11  keys: packed codes from the ring to a K tile (binary16,
+//               128-byte swizzle)
+//   warps 12-15 values: the same to a V tile (rows are elements: K-major along
+//               the positions, which is the order of the packed V tiles)
+//   warp 16     issues the MMAs (one lane)
+//   warp 17     walks the work list, publishes each piece of work, and copies
+//               the packed codes and parameters of 32 positions at a time into
+//               the ring (cp.async.bulk)
+//   warps 18-19 idle (registers are split by groups of four warps)
+// In a wide unit (more than 128 rows) the slots are its two halves and share
+// each K and V tile; in a narrow one they take alternate tiles of the same
+// rows and are merged at the end, so that one slot's softmax runs while the
+// other's products do.
+//
+// Work: units of up to UNIT rows of one kv head, each a number of steps (one
+// tile for both slots, or one tile a slot).  All units' steps are laid end to
+// end and every CTA takes an equal share, so that ragged lengths, few rows
+// with long contexts and more units than SMs all fill the card.  A unit cut by
+// a share's border leaves partial results (o, m, l) that combine_kernel joins;
+// whole units write their output directly.  The division depends on the
+// lengths and the grid alone, so results do not depend on timing.
+//
+// Bound: for wide units the tensor pipe and the exponentials together (128 x
+// 128 x D products take 512 cycles each, 128 x 128 exponentials 1024); for
+// narrow ones the tensor pipe at few valid rows, or HBM.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "serve.h"
+#include "tc.cuh"
+
+namespace kvq {
+namespace chunk {
+
+constexpr int kThreads = 20 * 32;
+constexpr int kWarpsK = 8, kWarpsV = 12, kWarpMma = 16, kWarpLoad = 17;
+// Registers a thread at launch, and of each warpgroup after the split: the
+// softmax groups take what the others give, 256 x 128 + 256 x 72 + 128 x 80
+// = 640 x 96.  (Five warps share an SM quarter's 16384 registers, hence 96.)
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsUnpack = 72, kRegsIssue = 80;
+static_assert(256 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThreads * kRegsLaunch,
+              "more registers than the launch has would never be granted");
+constexpr int kRing = 16;         // ring blocks at most
+constexpr int kBlock = 32;        // positions of a ring block
+constexpr int kSmemMax = 232448;  // shared memory a CTA may have (227 KB)
+constexpr int kHeader = 3 * 1024; // barriers, pieces, merge statistics
+
+template <int D_, int PIECES_, int NT_>
+struct Cfg {
+  static constexpr int D = D_, PIECES = PIECES_;
+  static constexpr int NT = NT_;                     // positions of a tile
+  static constexpr int KP = PIECES == 1 ? 1 : 2;     // pieces of a key or value
+  static constexpr int UNIT = unit_rows(PIECES);     // rows of a unit
+  static constexpr int HALVES = 128 / NT;            // warps that share a ring block
+  static constexpr int BLOCKS = NT / kBlock;
+  static constexpr int QTILE = 128 * D * 2;          // bytes of one Q region
+  static constexpr int KPIECE = NT * D * 2;
+  static constexpr int STAGE = KPIECE * KP;          // bytes of a K or V tile
+  static constexpr int SMEM_K = 2 * QTILE;
+  static constexpr int SMEM_V = SMEM_K + 2 * STAGE;
+  static constexpr int SMEM_RING = SMEM_V + 2 * STAGE;
+  // tensor memory columns: S (P in its place) and O of each slot
+  static constexpr int S_COL = 128, O_COL = 128, O_BASE = 256;
+  // weights are 2^(x - m + kOffset): their smallest binary16 values lie that
+  // much below the largest ones, which stay below 2^(kOffset + kThreshold)
+  static constexpr float kOffset = PIECES == 3 ? 11.0f : 7.0f;
+  static constexpr float kThreshold = PIECES == 3 ? 4.0f : 8.0f;
+};
+
+// One piece of work: steps [j0, j1) of a unit.
+struct Piece {
+  int valid, h, start, n, len;  // batch row: first packed token, tokens, length
+  int row0, rows, wide;         // unit's first row, number of rows
+  int lim;                      // positions that its last row sees
+  int t0, t1;                   // tiles the piece needs, [t0, t1)
+  int nt0;                      // wide: tiles of slot 0
+  int j0, j1;
+  int begin, end;               // whether it holds the unit's first and last step
+  int b;
+  int pad[15];
+};
+static_assert(sizeof(Piece) == 128, "");
+
+struct Shared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t q_full, m_full, m_free;
+  uint64_t d_full[2], d_empty[2];
+  uint64_t ring_full[kRing], ring_empty[kRing];
+  uint32_t tmem;
+  int abort;
+  int total;  // steps of one kv head's units
+  int pad;
+  Piece piece[2];
+  float2 stat[128];  // narrow merge: slot 1's (m, l)
+};
+static_assert(sizeof(Shared) <= kHeader - 1024, "header");
+
+struct Waiter {
+  uint32_t* err;
+  int* abort;
+  // Bounded wait of one thread: false if the phase did not complete within a
+  // second, or if another wait of this CTA gave up.
+  __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    return slow(bar, parity);
+  }
+  // The same for a whole warp, which takes one way.
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, one(bar, parity)) != 0;
+  }
+  __device__ __forceinline__ bool slow(uint64_t* bar, uint32_t parity) const {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*reinterpret_cast<volatile int*>(abort) != 0) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        flag_error(err, KVQ_DEVERR_TIMEOUT);
+        *reinterpret_cast<volatile int*>(abort) = 1;
+        return false;
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------- work
+// Tokens of batch row b; n = 0 if its offsets are not usable.
+struct RowInfo {
+  int start, n, len;
+  bool bad, longer;
+};
+
+__device__ __forceinline__ RowInfo row_info(const ChunkArgs& a, int b) {
+  RowInfo r;
+  r.start = __ldg(a.cu + b);
+  const int end = __ldg(a.cu + b + 1);
+  r.bad = r.start < 0 || end < r.start || end - r.start > a.max_q_len || end > a.num_tokens;
+  r.n = r.bad ? 0 : end - r.start;
+  const int lim = min(a.max_seq_len, a.capacity);
+  const int len = __ldg(a.seq_lens + b);
+  r.longer = len > lim;
+  r.len = max(0, min(len, lim));
+  return r;
+}
+
+// Positions that unit row r (of batch row tokens n, length len) sees.
+__device__ __forceinline__ int limit_of(const ChunkArgs& a, int n, int len, int r) {
+  return a.causal ? max(0, min(len, len - n + r / a.gq + 1)) : len;
+}
+
+struct Unit {
+  int row0, rows, wide, lim, nt, nt0, steps;
+};
+
+template <class C>
+__device__ __forceinline__ Unit unit_of(const ChunkArgs& a, int n, int len, int m) {
+  Unit u;
+  u.row0 = m * C::UNIT;
+  u.rows = min(C::UNIT, n * a.gq - u.row0);
+  u.wide = u.rows > 128;
+  u.lim = limit_of(a, n, len, u.row0 + u.rows - 1);
+  u.nt = (u.lim + C::NT - 1) / C::NT;
+  u.nt0 = u.wide ? (limit_of(a, n, len, u.row0 + 127) + C::NT - 1) / C::NT : 0;
+  u.steps = max(1, u.wide ? u.nt : (u.nt + 1) / 2);
+  return u;
+}
+
+// What a unit counts in the division of work.
+template <class C>
+__device__ __forceinline__ int unit_cost(const ChunkArgs& a, int n, int len, int m) {
+  return a.whole_units ? 1 : unit_of<C>(a, n, len, m).steps;
+}
+
+__device__ __forceinline__ int warp_sum(int v) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+__device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += u;
+  }
+  return v;
+}
+
+// Inclusive prefix sums of the rows' costs into pref[0 .. batch) (all warps;
+// ends with a CTA barrier); the errors of unusable rows are flagged once.
+template <class C>
+__device__ __forceinline__ void scan_rows(const ChunkArgs& a, int* pref, Shared* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool reports = blockIdx.x == 0;
+  if (a.max_units > 8) {  // long chunks: a warp per row
+    for (int b = warp; b < a.batch; b += kThreads / 32) {
+      const RowInfo r = row_info(a, b);
+      const int mt = (r.n * a.gq + C::UNIT - 1) / C::UNIT;
+      int c = 0;
+      for (int m = lane; m < mt; m += 32) c += unit_cost<C>(a, r.n, r.len, m);
+      c = warp_sum(c);
+      if (lane == 0) {
+        pref[b] = c;
+        if (reports && r.bad) flag_error(a.err, KVQ_DEVERR_BAD_POS);
+        if (reports && r.longer) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);
+      }
+    }
+  } else {
+    for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+      const RowInfo r = row_info(a, b);
+      const int mt = (r.n * a.gq + C::UNIT - 1) / C::UNIT;
+      int c = 0;
+      for (int m = 0; m < mt; ++m) c += unit_cost<C>(a, r.n, r.len, m);
+      pref[b] = c;
+      if (reports && r.bad) flag_error(a.err, KVQ_DEVERR_BAD_POS);
+      if (reports && r.longer) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const int s = before + warp_scan(b < a.batch ? pref[b] : 0, lane);
+      if (b < a.batch) pref[b] = s;
+      before = __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) sh->total = before;
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------- unpacking
+// binary16 pair of the codes at bits S (low half) and 16 + S (high half) of
+// w, S + B <= 8: the code's bits dropped into the mantissa of 2^(10 - S) (whose
+// last place is then worth 2^-S at bit 0, 1 at bit S), which is subtracted.
+template <int B, int S>
+__device__ __forceinline__ __half2 code_pair(uint32_t w) {
+  constexpr uint32_t mask = ((1u << B) - 1) << S;
+  constexpr uint32_t magic = 0x6400u - S * 0x400u;
+  uint32_t x = (w & (mask | (mask << 16))) | (magic | (magic << 16));
+  const uint32_t mm = magic | (magic << 16);
+  return __hsub2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&mm));
+}
+
+// The same for field e (0 .. 16/B - 1) of the halves.
+template <int B>
+__device__ __forceinline__ __half2 code_field(uint32_t w, int e) {
+  const int s = (B * e) & 7;
+  if (B * e >= 8) w >>= 8;
+  if constexpr (B == 8) {
+    return code_pair<8, 0>(w);
+  } else if constexpr (B == 4) {
+    return s == 0 ? code_pair<4, 0>(w) : code_pair<4, 4>(w);
+  } else {
+    return s == 0   ? code_pair<2, 0>(w)
+           : s == 2 ? code_pair<2, 2>(w)
+           : s == 4 ? code_pair<2, 4>(w)
+                    : code_pair<2, 6>(w);
+  }
+}
+
+// A group's (scale, zero) with the largest code's value inside binary16: the
+// stored roundings can push it past 65504 (by 2^-10 of its range at most);
+// the scale then gives up as many last places.
+template <int B>
+__device__ __forceinline__ uint32_t fit_params(uint32_t par) {
+  const float2 f = unpack_half2(par);
+  const float top = static_cast<float>((1 << B) - 1);
+  if (fmaf(top, f.x, f.y) > 65504.0f) {
+#pragma unroll 1
+    for (int i = 0; i < 4 && (par & 0xffffu) != 0; ++i) {
+      par -= 1;  // the next binary16 scale towards zero
+      const float2 g = unpack_half2(par);
+      if (fmaf(top, g.x, g.y) <= 65504.0f) break;
+    }
+  }
+  return par;
+}
+
+// hi and lo binary16 pairs of code * scale + zero, for two codes.
+template <int KP>
+__device__ __forceinline__ void value_pair(__half2 code, uint32_t scale2, uint32_t zero2,
+                                           uint32_t& hi, uint32_t& lo) {
+  if constexpr (KP == 1) {
+    const __half2 v = __hfma2(code, *reinterpret_cast<__half2*>(&scale2),
+                              *reinterpret_cast<__half2*>(&zero2));
+    hi = *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const float2 c = __half22float2(code), s = unpack_half2(scale2), z = unpack_half2(zero2);
+    const float x = fmaf(c.x, s.x, z.x), y = fmaf(c.y, s.y, z.y);
+    hi = f2_to_h2(x, y);
+    const float2 h = unpack_half2(hi);
+    lo = f2_to_h2(x - h.x, y - h.y);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  }
+}
+
+__device__ __forceinline__ void store_chunk(uint8_t* p, const uint32_t (&x)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// Keys of one ring block into rows of the K tile: one lane a position (row r
+// of the tile), elements [half * D / HALVES, + D / HALVES).
+template <class C, int B>
+__device__ __forceinline__ void unpack_keys(const uint8_t* codes, const uint32_t* params,
+                                            int group, int pos, int half, bool live,
+                                            uint8_t* tile, int r) {
+  constexpr int D = C::D, CU = D / 8 / C::HALVES, E = 16 / B;
+  constexpr int WORDS = CU >= E ? CU / E : 1;       // words of a slice this lane takes
+  constexpr int EW = CU >= E ? E : CU;              // units of a word it takes
+  constexpr int LOAD = WORDS < 4 ? WORDS : 4;       // words of one load
+  const int groups = D / group;
+  const uint8_t* row = codes + pos * (D * B / 8) + half * (WORDS * 4) * (CU >= E ? 1 : 0);
+  const int pre = CU >= E ? 0 : half * CU * B;      // first unit's field in the word
+  uint32_t scale2 = 0, zero2 = 0;
+#pragma unroll
+  for (int l = 0; l < WORDS / LOAD; ++l) {
+    uint32_t w[4][LOAD];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) load_words<LOAD>(row + c * (D * B / 32) + l * 16, w[c]);
+#pragma unroll
+    for (int i = 0; i < LOAD; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (CU < E) w[c][i] >>= pre;
+#pragma unroll
+      for (int e = 0; e < EW; ++e) {
+        const int uu = (l * LOAD + i) * E + e, u = half * CU + uu;
+        if (uu % 4 == 0 && (uu == 0 || ((8 * u) & (group - 1)) == 0)) {  // a group begins
+          uint32_t par = live ? fit_params<B>(params[pos * groups + 8 * u / group]) : 0u;
+          scale2 = __byte_perm(par, 0, 0x1010);
+          zero2 = __byte_perm(par, 0, 0x3232);
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          value_pair<C::KP>(code_field<B>(w[c][i], e), scale2, zero2, hi[c], lo[c]);
+        uint8_t* dst = tile + (u / 8) * (C::NT * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+        store_chunk(dst, hi);
+        if constexpr (C::KP == 2) store_chunk(dst + C::KPIECE, lo);
+      }
+    }
+  }
+}
+
+// Values of one ring block into columns of the V tile (its rows are elements,
+// 64 positions a 128-byte row): lane = 8 octet + m takes the elements 8u + m
+// of the octet's eight positions, u in [half * D/8 / HALVES, ...).
+template <class C, int B>
+__device__ __forceinline__ void unpack_values(const uint8_t* codes, const uint32_t* params,
+                                              int group, int lane, int half, int live,
+                                              uint8_t* tile, int octet0) {
+  constexpr int D = C::D, CU = D / 8 / C::HALVES, E = 16 / B;
+  constexpr int W = D * B / 128;                    // words of an octet in a format lane
+  constexpr int N = D * B / 16, P = N < 16 ? N : 16;
+  constexpr int WORDS = CU >= E ? CU / E : 1;
+  constexpr int EW = CU >= E ? E : CU;
+  constexpr int LOAD = WORDS < 4 ? WORDS : 4;
+  const int groups = D / group;
+  const int octet = lane >> 3, m = lane & 7;        // octet of the block: 0 .. 3
+  const uint8_t* base = codes + (octet >> 1) * (2 * D * B) + 4 * m * P;
+  const int q0 = (octet & 1) * W + (CU >= E ? half * WORDS : 0);  // first word
+  const int pre = CU >= E ? 0 : half * CU * B;
+  const int og = octet0 + octet;                    // octet of the tile
+  uint8_t* col = tile + (og >> 3) * (D * 128) + m * 128 + (((og & 7) ^ m) << 4);
+  uint32_t scale2[4], zero2[4];
+#pragma unroll
+  for (int l = 0; l < WORDS / LOAD; ++l) {
+    uint32_t w[4][LOAD];
+    const int n = 4 * (q0 + l * LOAD);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_words<LOAD>(base + (n / P) * (32 * P) + i * P + n % P, w[i]);
+#pragma unroll
+    for (int x = 0; x < LOAD; ++x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (CU < E) w[i][x] >>= pre;
+#pragma unroll
+      for (int e = 0; e < EW; ++e) {
+        const int uu = (l * LOAD + x) * E + e, u = half * CU + uu;
+        if (uu % 4 == 0 && (uu == 0 || ((8 * u) & (group - 1)) == 0)) {
+          const uint32_t* src = params + (octet * 8) * groups + 8 * u / group;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = octet * 8 + 2 * i;
+            const uint32_t p0 = k < live ? fit_params<B>(src[(2 * i) * groups]) : 0u;
+            const uint32_t p1 = k + 1 < live ? fit_params<B>(src[(2 * i + 1) * groups]) : 0u;
+            scale2[i] = __byte_perm(p0, p1, 0x5410);
+            zero2[i] = __byte_perm(p0, p1, 0x7632);
+          }
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          value_pair<C::KP>(code_field<B>(w[i][x], e), scale2[i], zero2[i], hi[i], lo[i]);
+        uint8_t* dst = col + u * (8 * 128);
+        store_chunk(dst, hi);
+        if constexpr (C::KP == 2) store_chunk(dst + C::KPIECE, lo);
+      }
+    }
+  }
+}
+
+// Positions that no row of the unit sees: zero, so that weights of 0 stay 0.
+template <class C, bool KEYS>
+__device__ __forceinline__ void zero_block(int lane, int half, uint8_t* tile, int blk) {
+  constexpr int CU = C::D / 8 / C::HALVES;
+  const uint32_t z[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int uu = 0; uu < CU; ++uu) {
+    const int u = half * CU + uu;
+    uint8_t* dst;
+    if (KEYS) {
+      const int r = blk * kBlock + lane;
+      dst = tile + (u / 8) * (C::NT * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+    } else {
+      const int og = blk * 4 + (lane >> 3), m = lane & 7;
+      dst = tile + (og >> 3) * (C::D * 128) + (8 * u + m) * 128 + (((og & 7) ^ m) << 4);
+    }
+    store_chunk(dst, z);
+    if (C::KP == 2) store_chunk(dst + C::KPIECE, z);
+  }
+}
+
+// ------------------------------------------------------------------- roles
+struct RingLayout {
+  int bytes, k, v, kp, vp;  // block size; offsets of its four arrays
+  int blocks;
+};
+
+__device__ __forceinline__ RingLayout ring_layout(const BlockCache& c, int avail) {
+  RingLayout l;
+  l.k = 0;
+  l.v = kBlock * c.head_dim * c.bits_k / 8;
+  l.kp = l.v + kBlock * c.head_dim * c.bits_v / 8;
+  l.vp = l.kp + kBlock * (c.head_dim / c.group) * 4;
+  l.bytes = l.vp + kBlock * (c.head_dim / c.group_v) * 4;
+  l.blocks = min(kRing, avail / l.bytes);
+  return l;
+}
+
+// Work list and copies (warp 17).
+template <class C>
+__device__ __forceinline__ bool load_role(const ChunkArgs& a, Shared* sh, uint8_t* ring,
+                                          const RingLayout& rl, const int* pref,
+                                          const Waiter& wait) {
+  const int lane = threadIdx.x & 31;
+  const int Wu = sh->total;
+  const long long W = static_cast<long long>(Wu) * a.c.kv_heads;
+  long long share = (W + gridDim.x - 1) / gridDim.x;
+  if (share < a.min_share) share = a.min_share;
+  long long w = share * blockIdx.x;
+  const long long w1 = min(W, w + share);
+  int piece = 0, slot = 0;
+  uint32_t phase = 0;
+  uint32_t headers = 0;  // partial slots that this CTA filled
+  bool ok = true;
+  if (w < w1) {
+    int h = static_cast<int>(w / Wu);
+    const int x0 = static_cast<int>(w - static_cast<long long>(h) * Wu);
+    int b, lo = 0, hi = a.batch;  // first row whose inclusive prefix exceeds x0
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pref[mid] > x0)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    b = lo;
+    RowInfo r = row_info(a, b);
+    int within = x0 - (b > 0 ? pref[b - 1] : 0);
+    int mt = (r.n * a.gq + C::UNIT - 1) / C::UNIT, m = 0;
+    __syncwarp();
+    while (true) {  // 32 units at a time
+      const int c = m + lane < mt ? unit_cost<C>(a, r.n, r.len, m + lane) : 0;
+      const int s = warp_scan(c, lane);
+      const uint32_t above = __ballot_sync(0xffffffffu, s > within);
+      if (above != 0) {
+        const int f = __ffs(above) - 1;
+        within -= __shfl_sync(0xffffffffu, s - c, f);
+        m += f;
+        break;
+      }
+      within -= __shfl_sync(0xffffffffu, s, 31);
+      m += 32;
+    }
+    int j = a.whole_units ? 0 : within;
+    while (ok && w < w1) {
+      const Unit u = unit_of<C>(a, r.n, r.len, m);
+      const int je = a.whole_units
+                         ? u.steps
+                         : static_cast<int>(min(static_cast<long long>(u.steps), j + (w1 - w)));
+      // publish the piece
+      ok = wait(&sh->d_empty[piece & 1], ((piece >> 1) & 1) ^ 1);
+      if (!ok) break;
+      const int t0 = u.wide ? j : min(u.nt, 2 * j), t1 = u.wide ? min(u.nt, je) : min(u.nt, 2 * je);
+      if (lane == 0) {
+        Piece& p = sh->piece[piece & 1];
+        p.valid = 1;
+        p.b = b; p.h = h; p.start = r.start; p.n = r.n; p.len = r.len;
+        p.row0 = u.row0; p.rows = u.rows; p.wide = u.wide; p.lim = u.lim;
+        p.t0 = t0; p.t1 = t1; p.nt0 = u.nt0;
+        p.j0 = j; p.j1 = je; p.begin = j == 0; p.end = je == u.steps;
+        mbar_arrive(&sh->d_full[piece & 1]);
+        if (!(p.begin && p.end)) {
+          int* hd = a.ws_head + (blockIdx.x * 2 + p.begin) * 8;
+          hd[0] = 1; hd[1] = r.start; hd[2] = h; hd[3] = u.row0; hd[4] = u.rows; hd[5] = p.end;
+          headers |= 1u << p.begin;
+        }
+      }
+      ++piece;
+      // copy its positions, 32 at a time; the pages of 32 blocks looked up at once
+      const int first = t0 * C::NT, last = min(u.lim, t1 * C::NT);
+      int page = 0;
+      for (int p = first, i = 0; p < last; p += kBlock, ++i) {
+        if ((i & 31) == 0) {
+          const int q = p + lane * kBlock;
+          page = b;
+          if (a.table != nullptr && q < last) {
+            page = __ldg(a.table + static_cast<size_t>(b) * a.pages_per_seq + (q >> a.page_shift));
+            if (page < 0 || page >= a.c.blocks) {
+              flag_error(a.err, KVQ_DEVERR_BAD_PAGE);
+              page = -1;
+            }
+          }
+        }
+        const int block = __shfl_sync(0xffffffffu, page, i & 31);
+        ok = wait(&sh->ring_empty[slot], phase ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          uint64_t* bar = &sh->ring_full[slot];
+          if (block < 0) {
+            mbar_arrive(bar);  // (that row's output is unspecified)
+          } else {
+            const int local = a.table != nullptr ? p & ((1 << a.page_shift) - 1) : p;
+            const int cnt = min(kBlock, (last - p + 15) & ~15);  // whole V tiles
+            const size_t row =
+                (static_cast<size_t>(block) * a.c.kv_heads + h) * a.c.block_tokens + local;
+            uint8_t* dst = ring + slot * rl.bytes;
+            const int kb = a.c.head_dim * a.c.bits_k / 8, vb = a.c.head_dim * a.c.bits_v / 8;
+            const int gk = a.c.head_dim / a.c.group, gv = a.c.head_dim / a.c.group_v;
+            mbar_arrive_expect_tx(bar, cnt * (kb + vb + 4 * gk + 4 * gv));
+            bulk_copy_g2s(dst + rl.k, a.c.k_codes + row * kb, cnt * kb, bar);
+            bulk_copy_g2s(dst + rl.kp, a.c.k_params + row * gk, cnt * gk * 4, bar);
+            bulk_copy_g2s(dst + rl.v, a.c.v_codes + row * vb, cnt * vb, bar);
+            bulk_copy_g2s(dst + rl.vp, a.c.v_params + row * gv, cnt * gv * 4, bar);
+          }
+        }
+        __syncwarp();
+        if (++slot == rl.blocks) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      w += a.whole_units ? 1 : je - j;
+      j = 0;
+      if (w < w1 && je == u.steps && ++m == mt) {  // the next row with tokens
+        m = 0;
+        ++b;
+        while (true) {
+          if (b >= a.batch) {
+            b = 0;
+            ++h;
+          }
+          const int c = b + lane;
+          const bool has = c < a.batch && row_info(a, c).n > 0;
+          const uint32_t some = __ballot_sync(0xffffffffu, has);
+          if (some != 0) {
+            b += __ffs(some) - 1;
+            break;
+          }
+          b += 32;
+        }
+        r = row_info(a, b);
+        mt = (r.n * a.gq + C::UNIT - 1) / C::UNIT;
+      }
+    }
+  }
+  // the end of the list, and the partial slots that stay empty
+  if (ok) ok = wait(&sh->d_empty[piece & 1], ((piece >> 1) & 1) ^ 1);
+  if (lane == 0) {
+    if (ok) {
+      sh->piece[piece & 1].valid = 0;
+      mbar_arrive(&sh->d_full[piece & 1]);
+    }
+    if (!a.whole_units) {
+      if (!(headers & 1u)) a.ws_head[(blockIdx.x * 2 + 0) * 8] = 0;
+      if (!(headers & 2u)) a.ws_head[(blockIdx.x * 2 + 1) * 8] = 0;
+    }
+    // copies in flight end before the CTA does: a block is refilled only
+    // after it was waited for, so only the last ones can be pending
+    if (!ok) {
+      for (int i = 0; i < rl.blocks; ++i) {
+        const int s = (slot + i) % rl.blocks;
+        const uint32_t ph = s >= slot ? phase ^ 1 : phase;
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(&sh->ring_full[s], ph) && global_timer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+  }
+  __syncwarp();
+  return ok;
+}
+
+// Unpacking (warps 8-15).
+template <class C, bool KEYS, int B>
+__device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint8_t* tiles,
+                                            const uint8_t* ring, const RingLayout& rl,
+                                            const Waiter& wait) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+  const int blk = w / C::HALVES, half = w % C::HALVES;
+  uint64_t* full = KEYS ? sh->k_full : sh->v_full;
+  uint64_t* empty = KEYS ? sh->k_empty : sh->v_empty;
+  const int group = KEYS ? a.c.group : a.c.group_v;
+  int slot = 0, tile = 0;
+  uint32_t phase = 0;
+  for (int piece = 0;; ++piece) {
+    if (!wait(&sh->d_full[piece & 1], (piece >> 1) & 1)) return false;
+    const Piece& p = sh->piece[piece & 1];
+    if (!p.valid) return true;
+    const int t0 = p.t0, t1 = p.t1, lim = p.lim;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->d_empty[piece & 1]);
+    for (int t = t0; t < t1; ++t, ++tile) {
+      const int used = min(C::BLOCKS, (lim - t * C::NT + kBlock - 1) / kBlock);
+      uint8_t* dst = tiles + (tile & 1) * C::STAGE;
+      if (!wait(&empty[tile & 1], ((tile >> 1) & 1) ^ 1)) return false;
+      // A phase bit tells one use of a ring block from the next only: the use
+      // before this one must be filled.  It is a block of an earlier tile
+      // (the ring holds a tile), so with a short ring that tile is waited for.
+      if (rl.blocks < 2 * C::BLOCKS && tile > 0 &&
+          !wait(&full[(tile - 1) & 1], ((tile - 1) >> 1) & 1))
+        return false;
+      if (blk < used) {
+        int s = slot + blk;
+        uint32_t ph = phase;
+        if (s >= rl.blocks) {
+          s -= rl.blocks;
+          ph ^= 1;
+        }
+        if (!wait(&sh->ring_full[s], ph)) return false;
+        const uint8_t* src = ring + s * rl.bytes;
+        const int live = lim - t * C::NT - blk * kBlock;  // positions of the block that are seen
+        if constexpr (KEYS)
+          unpack_keys<C, B>(src + rl.k, reinterpret_cast<const uint32_t*>(src + rl.kp), group,
+                            lane, half, lane < live, dst, blk * kBlock + lane);
+        else
+          unpack_values<C, B>(src + rl.v, reinterpret_cast<const uint32_t*>(src + rl.vp), group,
+                              lane, half, live, dst, blk * 4);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->ring_empty[s]);
+      } else {
+        zero_block<C, KEYS>(lane, half, dst, blk);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[tile & 1]);
+      slot += used;
+      while (slot >= rl.blocks) {
+        slot -= rl.blocks;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+// MMA issue (warp 16, one lane).
+template <class C>
+__device__ __forceinline__ void issue_scores(uint32_t s_tmem, uint32_t q, uint32_t k) {
+  constexpr uint32_t idesc = tc::idesc_f16_kk(128, C::NT);
+  // (Q piece, K piece) products; small ones first
+  constexpr int terms = C::PIECES;
+#pragma unroll
+  for (int x = terms - 1; x >= 0; --x) {
+    const uint32_t qa = q + (x == 2 ? C::QTILE : 0), ka = k + (x == 1 ? C::KPIECE : 0);
+#pragma unroll
+    for (int i = 0; i < C::D / 16; ++i)
+      tc::mma_f16_ss(s_tmem, tc::smem_desc_k128(qa + (i / 4) * (128 * 128) + (i % 4) * 32),
+                     tc::smem_desc_k128(ka + (i / 4) * (C::NT * 128) + (i % 4) * 32), idesc,
+                     !(x == terms - 1 && i == 0));
+  }
+}
+
+template <class C>
+__device__ __forceinline__ void issue_output(uint32_t o_tmem, uint32_t p_tmem, uint32_t v,
+                                             bool accumulate) {
+  constexpr uint32_t idesc = tc::idesc_f16_kk(128, C::D);
+  constexpr int terms = C::PIECES;
+#pragma unroll
+  for (int x = terms - 1; x >= 0; --x) {
+    const uint32_t pa = p_tmem + (x == 2 ? C::NT / 2 : 0), va = v + (x == 1 ? C::KPIECE : 0);
+#pragma unroll
+    for (int i = 0; i < C::NT / 16; ++i)
+      tc::mma_f16_ts(o_tmem, pa + i * 8,
+                     tc::smem_desc_k128(va + (i / 4) * (C::D * 128) + (i % 4) * 32), idesc,
+                     accumulate || !(x == terms - 1 && i == 0));
+  }
+}
+
+template <class C>
+__device__ __forceinline__ bool mma_role(Shared* sh, uint32_t smem, uint32_t tmem,
+                                         const Waiter& wait) {
+  int tile0 = 0;                      // tiles of the pieces before
+  uint32_t p_phase[2] = {0, 0};
+  for (int piece = 0;; ++piece) {
+    if (!wait.one(&sh->d_full[piece & 1], (piece >> 1) & 1)) return false;
+    const Piece p = sh->piece[piece & 1];
+    if (!p.valid) return true;
+    mbar_arrive(&sh->d_empty[piece & 1]);
+    // slot s works in step j iff active(s, j); on tile tile_of(s, j)
+    auto active = [&](int s, int j) {
+      return j < p.j1 && (p.wide ? (s == 1 ? j < p.t1 : j < p.nt0) : 2 * j + s < p.t1);
+    };
+    auto index = [&](int s, int j) { return tile0 + (p.wide ? j : 2 * j + s) - p.t0; };
+    // queries are needed before the first scores, a K tile by its first user
+    if (!wait.one(&sh->q_full, piece & 1)) return false;
+    int k_seen = tile0;               // K tiles waited for
+    auto scores = [&](int s, int j) {
+      const int t = index(s, j);
+      if (t == k_seen) {
+        if (!wait.one(&sh->k_full[t & 1], (t >> 1) & 1)) return false;
+        ++k_seen;
+      }
+      tc::fence_after_sync();
+      const uint32_t q = smem + (p.wide && s == 1 ? C::QTILE : 0);
+      issue_scores<C>(tmem + s * C::S_COL, q, smem + C::SMEM_K + (t & 1) * C::STAGE);
+      tc::commit(&sh->s_full[s]);
+      if (!p.wide || s == 1) tc::commit(&sh->k_empty[t & 1]);
+      return true;
+    };
+    for (int s = 0; s < 2; ++s)
+      if (active(s, p.j0) && !scores(s, p.j0)) return false;
+    int v_seen = tile0;
+    for (int j = p.j0; j < p.j1; ++j) {
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s) {
+        if (!active(s, j)) continue;
+        const int t = index(s, j);
+        if (!wait.one(&sh->p_full[s], p_phase[s])) return false;
+        p_phase[s] ^= 1;
+        if (t == v_seen) {
+          if (!wait.one(&sh->v_full[t & 1], (t >> 1) & 1)) return false;
+          ++v_seen;
+        }
+        tc::fence_after_sync();
+        issue_output<C>(tmem + C::O_BASE + s * C::O_COL, tmem + s * C::S_COL,
+                        smem + C::SMEM_V + (t & 1) * C::STAGE, j > p.j0);
+        if (!p.wide || s == 1) tc::commit(&sh->v_empty[t & 1]);
+        if (active(s, j + 1)) {
+          if (!scores(s, j + 1)) return false;
+        } else {
+          tc::commit(&sh->s_full[s]);  // the slot's output is complete
+        }
+      }
+    }
+    tile0 += p.t1 - p.t0;
+  }
+}
+
+// One row of queries as binary16 (two pieces for PIECES 3), scaled by a power
+// of two that brings its largest magnitude to [2^14, 2^15): bf16 and f16 rows
+// stay exact down to 2^-28 of the largest element.  Returns the factor that
+// undoes it.
+template <class C, bool ROT>
+__device__ __forceinline__ float load_query(const ChunkArgs& a, size_t off, bool valid,
+                                            uint8_t* q, int r) {
+  constexpr int D = C::D;
+  auto load8 = [&](int i, float (&x)[8]) {
+    if (!valid) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = 0.0f;
+    } else if (a.q_dtype == KVQ_F32) {
+      Load8<float>::run(static_cast<const float*>(a.q) + off + 8 * i, x);
+    } else if (a.q_dtype == KVQ_BF16) {
+      Load8<__nv_bfloat16>::run(static_cast<const __nv_bfloat16*>(a.q) + off + 8 * i, x);
+    } else {
+      Load8<__half>::run(static_cast<const __half*>(a.q) + off + 8 * i, x);
+    }
+  };
+  auto scale_of = [](float amax, float& up) {
+    int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127 - 14;
+    e = max(e, -126);
+    up = pow2i(-e);      // e <= 114
+    return pow2i(e);
+  };
+  auto put = [&](int u, const float (&x)[8], float up) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float y0 = x[2 * c] * up, y1 = x[2 * c + 1] * up;
+      hi[c] = f2_to_h2(y0, y1);
+      if constexpr (C::PIECES == 3) {
+        const float2 h = unpack_half2(hi[c]);
+        lo[c] = f2_to_h2(y0 - h.x, y1 - h.y);
+      }
+    }
+    uint8_t* dst = q + (u / 8) * (128 * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+    store_chunk(dst, hi);
+    if constexpr (C::PIECES == 3) store_chunk(dst + C::QTILE, lo);
+  };
+  float amax = 0.0f, up;
+  if constexpr (ROT) {  // H q / D, the butterfly h = 1, 2, ..., D/2
+    float x[D];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) load8(i, *reinterpret_cast<float(*)[8]>(x + 8 * i));
+#pragma unroll
+    for (int h = 1; h < D; h *= 2)
+#pragma unroll
+      for (int i = 0; i < D; ++i)
+        if ((i & h) == 0) {
+          const float y = x[i], z = x[i + h];
+          x[i] = y + z;
+          x[i + h] = y - z;
+        }
+#pragma unroll
+    for (int i = 0; i < D; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    const float down = scale_of(amax, up);
+#pragma unroll
+    for (int u = 0; u < D / 8; ++u) put(u, *reinterpret_cast<float(*)[8]>(x + 8 * u), up);
+    return down * (1.0f / D);
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      float x[8];
+      load8(i, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
+    }
+    const float down = scale_of(amax, up);
+#pragma unroll 4
+    for (int u = 0; u < D / 8; ++u) {
+      float x[8];
+      load8(u, x);
+      put(u, x, up);
+    }
+    return down;
+  }
+}
+
+// Eight consecutive output elements.
+__device__ __forceinline__ void store_out8(void* out, int dtype, size_t i, const float (&x)[8]) {
+  if (dtype == KVQ_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + i);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (dtype == KVQ_BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * c], x[2 * c + 1]);
+        w[c] = *reinterpret_cast<uint32_t*>(&h);
+      } else {
+        w[c] = f2_to_h2(x[2 * c], x[2 * c + 1]);
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Softmax of one slot (warps 0-3: slot 0, 4-7: slot 1).
+template <class C, bool ROT>
+__device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uint8_t* smem,
+                                             uint32_t tmem, const Waiter& wait) {
+  constexpr int D = C::D, NT = C::NT;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int slot = warp >> 2, r = threadIdx.x & 127;  // row of the slot
+  const uint32_t quad = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t s_tmem = tmem + quad + slot * C::S_COL;
+  const uint32_t o_tmem = tmem + quad + C::O_BASE + slot * C::O_COL;
+  uint32_t s_phase = 0, merges = 0;
+  for (int piece = 0;; ++piece) {
+    if (!wait(&sh->d_full[piece & 1], (piece >> 1) & 1)) return false;
+    const Piece& pd = sh->piece[piece & 1];
+    if (!pd.valid) return true;
+    const bool wide = pd.wide;
+    const int t0 = pd.t0, t1 = pd.t1, nt0 = pd.nt0, j0 = pd.j0;
+    const int rows = pd.rows, ur = wide ? slot * 128 + r : r;  // row of the unit
+    const bool valid = ur < rows;
+    const bool whole = pd.begin && pd.end;
+    const int br = pd.row0 + (valid ? ur : 0);                 // row of the batch row
+    const int token = pd.start + br / a.gq, head = pd.h * a.gq + br % a.gq;
+    const int limit = valid ? limit_of(a, pd.n, pd.len, br) : 0x7fffffff;
+    const int part = pd.begin;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->d_empty[piece & 1]);
+    // the slot's tiles of this piece: t, t + stride, ... < tend
+    int t, tend, stride;
+    if (wide) {
+      t = t0; tend = slot == 0 ? min(t1, nt0) : t1; stride = 1;
+    } else {
+      t = 2 * j0 + slot; tend = t1; stride = 2;
+    }
+    const bool any_tile = t < tend;
+    const bool works = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps pace
+    // ---- queries
+    float unscale = 1.0f;
+    if (wide || slot == 0) {
+      if (works)
+        unscale = load_query<C, ROT>(
+            a, static_cast<size_t>(token) * a.q_stride + static_cast<size_t>(head) * D, valid,
+            smem + (wide ? slot * C::QTILE : 0), r);
+      fence_proxy_async_shared();
+    }
+    if (!wide && slot == 0) sh->stat[r].x = unscale;  // slot 1 has the same rows
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->q_full);
+    if (!wide && slot == 1) {
+      if (!wait(&sh->q_full, piece & 1)) return false;
+      unscale = sh->stat[r].x;
+    }
+    // scores in units of log2: S * c
+    const float c = fmaxf(a.sm_scale_log2 * unscale, 1.2e-38f);
+    float m = -INFINITY, l = 0.0f;
+    for (bool first = true; t < tend; t += stride, first = false) {
+      if (!wait(&sh->s_full[slot], s_phase)) return false;
+      s_phase ^= 1;
+      tc::fence_after_sync();
+      if (works) {
+        // the scores are read twice, 32 columns at a time, for their maximum
+        // and for the weights: held in registers (NT of them) they spill
+        const int seen = limit - t * NT;
+        const bool masks = __any_sync(0xffffffffu, seen < NT);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) {
+          uint32_t s[32];
+          tc::ld_32x32b<32>(s_tmem + 32 * i, s);
+          tc::wait_ld(s);
+          if (masks) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * i + k >= seen) s[k] = 0xff800000u;  // -inf
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
+        }
+        mx = fmaxf(mx, m);
+        const bool grown = (mx - m) * c > C::kThreshold;  // (false while nothing is seen)
+        if (first) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, grown)) {
+          // every row moves to its maximum; its sums follow
+          const float f = mx == -INFINITY ? 1.0f : exp2_approx((m - mx) * c);
+          l *= f;
+          m = mx;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tc::ld_32x32b<32>(o_tmem + 32 * i, o);
+            tc::wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tc::st_32x32b_x32(o_tmem + 32 * i, o);
+          }
+        }
+        const float shift = C::kOffset - (m == -INFINITY ? 0.0f : m * c);
+        float l0 = 0.0f, l1 = 0.0f;
+        // (two binary16 pieces take a score's column each: all scores are read
+        // before the first are written; one piece's columns trail the reads)
+        constexpr int HELD = C::PIECES == 3 ? NT : 32;
+#pragma unroll
+        for (int h = 0; h < NT / HELD; ++h) {
+          uint32_t s[HELD];
+#pragma unroll
+          for (int i = 0; i < HELD / 32; ++i)
+            tc::ld_32x32b<32>(s_tmem + HELD * h + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+#pragma unroll
+          for (int i = 0; i < HELD / 32; ++i)
+            tc::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+          if (masks) {
+#pragma unroll
+            for (int k = 0; k < HELD; ++k)
+              if (HELD * h + k >= seen) s[k] = 0xff800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < HELD / 32; ++i) {
+            uint32_t p[16], q[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float x = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k]), c, shift));
+              const float y = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k + 1]), c, shift));
+              l0 += x;
+              l1 += y;
+              p[k] = f2_to_h2(x, y);
+              if constexpr (C::PIECES == 3) {
+                const float2 hh = unpack_half2(p[k]);
+                q[k] = f2_to_h2(x - hh.x, y - hh.y);
+              }
+            }
+            tc::st_32x32b_x16(s_tmem + HELD / 2 * h + 16 * i, p);
+            if constexpr (C::PIECES == 3) tc::st_32x32b_x16(s_tmem + NT / 2 + 16 * i, q);
+          }
+        }
+        l += l0 + l1;
+        tc::wait_st();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[slot]);
+    }
+    // ---- the slot's output
+    if (any_tile) {
+      if (!wait(&sh->s_full[slot], s_phase)) return false;
+      s_phase ^= 1;
+      tc::fence_after_sync();
+    }
+    float f0 = 1.0f, f1 = 0.0f;
+    float4* merge = reinterpret_cast<float4*>(smem) + r * (D / 4);  // slot 1's row, swizzled
+    const bool other = !wide && 2 * j0 + 1 < t1;                    // slot 1 has an output
+    if (!wide) {
+      if (slot == 1) {
+        if (other && works) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tc::ld_32x32b<32>(o_tmem + 32 * i, o);
+            tc::wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              merge[(8 * i + k) ^ (r & 7)] =
+                  make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                              __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+        }
+        sh->stat[r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->m_full);
+      } else {
+        if (!wait(&sh->m_full, merges & 1)) return false;
+        const float2 st = sh->stat[r];
+        const float mm = fmaxf(m, st.x), base = mm == -INFINITY ? 0.0f : mm;
+        f0 = exp2_approx((m - base) * c);
+        f1 = exp2_approx((st.x - base) * c);
+        l = l * f0 + st.y * f1;
+        m = mm;
+      }
+    }
+    if ((wide || slot == 0) && works) {
+      float* po = nullptr;
+      if (whole) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        f0 *= inv;
+        f1 *= inv;
+      } else {
+        const size_t prow = static_cast<size_t>(blockIdx.x * 2 + part) * a.part_rows + ur;
+        po = a.ws_o + prow * D;
+        if (valid) a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, l);
+      }
+      const size_t orow = (static_cast<size_t>(token) * a.q_heads + head) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        if (any_tile) {
+          tc::ld_32x32b<32>(o_tmem + 32 * i, o);
+          tc::wait_ld(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * k + e]) * f0;
+          if (other) {
+            const float4 y = merge[(8 * i + 2 * k) ^ (r & 7)], z = merge[(8 * i + 2 * k + 1) ^ (r & 7)];
+            x[0] = fmaf(y.x, f1, x[0]); x[1] = fmaf(y.y, f1, x[1]);
+            x[2] = fmaf(y.z, f1, x[2]); x[3] = fmaf(y.w, f1, x[3]);
+            x[4] = fmaf(z.x, f1, x[4]); x[5] = fmaf(z.y, f1, x[5]);
+            x[6] = fmaf(z.z, f1, x[6]); x[7] = fmaf(z.w, f1, x[7]);
+          }
+          if (valid) {
+            if (whole) {
+              if (!(l > 0.0f)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+              }
+              store_out8(a.out, a.out_dtype, orow + 32 * i + 8 * k, x);
+            } else {
+              float4* d = reinterpret_cast<float4*>(po + 32 * i + 8 * k);
+              d[0] = make_float4(x[0], x[1], x[2], x[3]);
+              d[1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
+          }
+        }
+      }
+    }
+    tc::fence_before_sync();
+    if (!wide) {  // the merge buffer is the query tiles' memory
+      __syncwarp();
+      if (slot == 0 && lane == 0) mbar_arrive(&sh->m_free);
+      if (!wait(&sh->m_free, merges & 1)) return false;
+      ++merges;
+    }
+  }
+}
+
+template <class C, bool ROT>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = smem + C::SMEM_RING;
+  Shared* sh = reinterpret_cast<Shared*>(smem + kSmemMax - kHeader);
+  const RingLayout rl = ring_layout(a.c, kSmemMax - kHeader - C::SMEM_RING);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->k_full[i], 4);
+      mbar_init(&sh->k_empty[i], 1);
+      mbar_init(&sh->v_full[i], 4);
+      mbar_init(&sh->v_empty[i], 1);
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], 4);
+      mbar_init(&sh->d_full[i], 1);
+      mbar_init(&sh->d_empty[i], 17);  // softmax 8, keys 4, values 4, MMA 1
+    }
+    mbar_init(&sh->q_full, 8);
+    mbar_init(&sh->m_full, 4);
+    mbar_init(&sh->m_free, 4);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh->ring_full[i], 1);
+      mbar_init(&sh->ring_empty[i], 2 * C::HALVES);
+    }
+    sh->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) {
+    tc::alloc(&sh->tmem, 512);
+    tc::relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  int* pref = reinterpret_cast<int*>(smem);  // (the tiles' memory is not yet in use)
+  scan_rows<C>(a, pref, sh);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  const Waiter wait{a.err, &sh->abort};
+
+  if (warp < kWarpsK) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax_role<C, ROT>(a, sh, smem, tmem, wait);
+  } else if (warp < kWarpMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+    if (warp < kWarpsV) {
+      uint8_t* tiles = smem + C::SMEM_K;
+      if (a.c.bits_k == 2)
+        unpack_role<C, true, 2>(a, sh, tiles, ring, rl, wait);
+      else if (a.c.bits_k == 4)
+        unpack_role<C, true, 4>(a, sh, tiles, ring, rl, wait);
+      else
+        unpack_role<C, true, 8>(a, sh, tiles, ring, rl, wait);
+    } else {
+      uint8_t* tiles = smem + C::SMEM_V;
+      if (a.c.bits_v == 2)
+        unpack_role<C, false, 2>(a, sh, tiles, ring, rl, wait);
+      else if (a.c.bits_v == 4)
+        unpack_role<C, false, 4>(a, sh, tiles, ring, rl, wait);
+      else
+        unpack_role<C, false, 8>(a, sh, tiles, ring, rl, wait);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kWarpMma) {
+      if ((threadIdx.x & 31) == 0) mma_role<C>(sh, smem_addr(smem), tmem, wait);
+      __syncwarp();
+    } else if (warp == kWarpLoad) {
+      load_role<C>(a, sh, ring, rl, pref, wait);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc::fence_after_sync();
+    if (sh->abort != 0) {  // (products in flight end before their memory is given back)
+      if ((threadIdx.x & 31) == 0) {
+        mbar_init(&sh->q_full, 1);
+        fence_barrier_init();
+        tc::commit(&sh->q_full);
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(&sh->q_full, 0) && global_timer_ns() - t0 < 10000000ull) {
+        }
+      }
+      __syncwarp();
+    }
+    tc::dealloc(tmem, 512);
+  }
+}
+
+}  // namespace chunk
+}  // namespace kvq

@@ -53,6 +53,17 @@ struct RaggedArgs {
 cudaError_t launch_append_ragged(const RaggedArgs& a, cudaStream_t stream);
 cudaError_t launch_dequantize_ragged(const RaggedArgs& a, cudaStream_t stream);
 
+// Chunk attention: binary16 pieces of an operand (1 to 3, see chunk.cuh), and
+// what follows from it: rows of a unit of work and positions of a tile.
+constexpr int unit_rows(int pieces) { return pieces == 3 ? 128 : 256; }
+// (8-bit keys and values of head_dim 128 leave no room for a ring of four
+// blocks beside tiles of 128)
+constexpr int tile_tokens(int pieces, int head_dim, int bits_kv) {
+  return pieces == 1 && !(head_dim == 128 && bits_kv == 16) ? 128 : 64;
+}
+// Batch rows one call takes (their prefix sums lie in the tiles' memory).
+constexpr int kChunkRows = 16384;
+
 struct ChunkArgs {
   BlockCache c;
   const int32_t* table;  // block table (NULL: slot layout)
@@ -69,8 +80,18 @@ struct ChunkArgs {
   void* out;
   int out_dtype;
   uint32_t* err;
+  // division of work: a CTA takes at least min_share steps, or whole units
+  bool whole_units;
+  int min_share;
+  int max_units;  // units of a batch row, at most
+  // partial results of units cut by a share's border, two places per CTA
+  // (0: a piece that continues a unit, 1: one that begins it)
+  int part_rows;  // rows of a place
+  int* ws_head;   // [grid][2][8]: valid, first token, kv head, first row, rows, last piece
+  float2* ws_ml;  // [grid][2][part_rows]: (reference exponent, sum)
+  float* ws_o;    // [grid][2][part_rows][D]
 };
 
-cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream);
+cudaError_t launch_chunk(const ChunkArgs& a, int pieces, int grid, cudaStream_t stream);
 
 }  // namespace kvq

@@ -102,12 +102,14 @@ def fill(cache, users, lens, seed, dtype="bf16", centre=0.0):
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 
 
-def attention_reference(q, kd, vd, cu_kv, cu_q, lens, causal, scale, out_dtype):
+def attention_reference(q, kd, vd, cu_kv, cu_q, lens, causal, scale, out_dtype, rot=False):
     """(o, tolerance) in 64 bits, both [T][Hq][D].
 
     Tolerance, for a kernel that takes binary16 operands and binary32 sums.
     With a query of 16-bit type exact, of binary32 to e_q = 2^-22 (two
-    halves); keys and values rounded once to binary16, e_k = e_v = 2^-11, for
+    halves), of a rotated cache, where it is a sum H q / D, rounded like one
+    (bf16 once, 2^-11; others in two halves; the products are then those of
+    the rotated vectors); keys and values rounded once to binary16, e_k = e_v = 2^-11, for
     bf16 queries, held in two halves (2^-22) otherwise; weights e_p = 2^-11,
     2^-22 for binary32.  Roundings are independent and bounded, so by
     Hoeffding's inequality a sum of them stays within z times the root of the
@@ -129,6 +131,11 @@ def attention_reference(q, kd, vd, cu_kv, cu_q, lens, causal, scale, out_dtype):
     tol = torch.zeros_like(out)
     kind = q.dtype
     e_q = 2.0 ** -22 if kind == torch.float32 else 0.0
+    if rot:
+        e_q = 2.0 ** -11 if kind == torch.bfloat16 else 2.0 ** -22
+        H = torch.ones(1, 1, dtype=torch.float64, device=q.device)
+        while H.shape[0] < D:
+            H = torch.cat([torch.cat([H, H], 1), torch.cat([H, -H], 1)], 0)
     e_kv = 2.0 ** -11 if kind == torch.bfloat16 else 2.0 ** -22
     e_p = 2.0 ** -22 if kind == torch.float32 else 2.0 ** -11
     z = 7.0
@@ -139,9 +146,13 @@ def attention_reference(q, kd, vd, cu_kv, cu_q, lens, causal, scale, out_dtype):
             continue
         k = kd[cu_kv[b]:cu_kv[b] + L].double().repeat_interleave(gq, 1)
         v = vd[cu_kv[b]:cu_kv[b] + L].double().repeat_interleave(gq, 1)
+        if rot:
+            k = k @ H
         for i0 in range(0, n, 128):
             sl = slice(cu_q[b] + i0, cu_q[b] + min(n, i0 + 128))
             x = q[sl].double()
+            if rot:
+                x = x @ H / D
             i = torch.arange(i0, min(n, i0 + 128), device=q.device)
             seen = (L - n + i + 1 if causal else torch.full_like(i, L)).clamp(0, L)
             if L == 0:

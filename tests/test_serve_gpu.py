@@ -273,7 +273,8 @@ def _chunk_case(lens, n_new, Hq, Hkv, D, bits, G, gv, P, rot, dtype, causal, see
     assert kvq.kvq_device_error_flags() == 0
     assert got is out
     assert (out[cu[-1]:] == 7.0).all()  # rows behind the last sequence
-    want, tol = attention_reference(q[:cu[-1]], kd, vd, cu_kv, cu, lens, causal, scale, out.dtype)
+    want, tol = attention_reference(q[:cu[-1]], kd, vd, cu_kv, cu, lens, causal, scale, out.dtype,
+                                    rot)
     assert_close(out[:cu[-1]], want, tol)
 
 
@@ -448,10 +449,9 @@ def test_single_tokens_agree_with_decode():
         # idle rows and single tokens, by the general path
         b = kvq.kvq_chunk_attention(cache, q[:3].contiguous(), i32([0, 1, 1, 2, 3]), i32(lens),
                                     1, 2000)
-        pick = [0, 2, 3]
         q3, cu3 = q[:3], [0, 1, 1, 2, 3]
         want, tol = attention_reference(q3, kd, vd, cu_kv, cu3, lens, True, 0.0, q.dtype)
-        assert_close(b, want, tol), pick
+        assert_close(b, want, tol)
 
 
 # ------------------------------------------------------------- all together
@@ -502,7 +502,7 @@ def test_serving_steps(P, dtype, rot):
         for x in allk:
             at.append(at[-1] + x.shape[0])
         want, tol = attention_reference(q, torch.cat(allk), torch.cat(allv), at, c, new, True, 0.0,
-                                        q.dtype)
+                                        q.dtype, rot)
         assert_close(out, want, tol)
         # some draft tokens are rejected, row 2 finishes in step 4
         back = [max(o, n - r.randint(0, 3)) if n - o == 4 else n for o, n in zip(old, new)]
