@@ -24,6 +24,8 @@ BlockCache block_cache(const kvq_cache_desc* c) {
   b.bits_v = c->bits_v;
   b.group = c->group;
   b.group_v = group_v_of(c);
+  b.gshift_k = b.group == 32 ? 5 : b.group == 64 ? 6 : 7;
+  b.gshift_v = b.group_v == 32 ? 5 : b.group_v == 64 ? 6 : 7;
   const bool paged = (c->flags & KVQ_FLAG_PAGED) != 0;
   b.blocks = paged ? c->num_pages : c->batch;
   b.block_tokens = paged ? c->page_size : c->capacity;

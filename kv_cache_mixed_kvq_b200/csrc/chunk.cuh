@@ -30,7 +30,7 @@
 //               128-byte swizzle)
 //   warps 12-15 values: the same to a V tile (rows are elements: K-major along
 //               the positions, which is the order of the packed V tiles)
-//   warp 16     issues the MMAs (one lane)
+//   warp 16     issues the MMAs
 //   warp 17     walks the work list, publishes each piece of work, and copies
 //               the packed codes and parameters of 32 positions at a time into
 //               the ring (cp.async.bulk)
@@ -64,15 +64,15 @@ namespace chunk {
 constexpr int kThreads = 20 * 32;
 constexpr int kWarpsK = 8, kWarpsV = 12, kWarpMma = 16, kWarpLoad = 17;
 // Registers a thread at launch, and of each warpgroup after the split: the
-// softmax groups take what the others give, 256 x 128 + 256 x 72 + 128 x 80
+// softmax groups take what the others give, 256 x 144 + 256 x 64 + 128 x 64
 // = 640 x 96.  (Five warps share an SM quarter's 16384 registers, hence 96.)
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsUnpack = 72, kRegsIssue = 80;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsUnpack = 64, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThreads * kRegsLaunch,
               "more registers than the launch has would never be granted");
 constexpr int kRing = 16;         // ring blocks at most
 constexpr int kBlock = 32;        // positions of a ring block
 constexpr int kSmemMax = 232448;  // shared memory a CTA may have (227 KB)
-constexpr int kHeader = 3 * 1024; // barriers, pieces, merge statistics
+constexpr int kHeader = 2 * 1024; // barriers, pieces, merge statistics
 
 template <int D_, int PIECES_, int NT_>
 struct Cfg {
@@ -123,32 +123,29 @@ struct Shared {
   Piece piece[2];
   float2 stat[128];  // narrow merge: slot 1's (m, l)
 };
-static_assert(sizeof(Shared) <= kHeader - 1024, "header");
+static_assert(sizeof(Shared) <= kHeader, "header");
 
 struct Waiter {
-  uint32_t* err;
   int* abort;
-  // Bounded wait of one thread: false if the phase did not complete within a
-  // second, or if another wait of this CTA gave up.
-  __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
-    return slow(bar, parity);
-  }
-  // The same for a whole warp, which takes one way.
+  // Bounded wait of a warp: false if the phase did not complete within a
+  // second, or if another wait of this CTA gave up (the kernel's end flags it).
+  // The loop is short: it is part of every role's code.
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, one(bar, parity)) != 0;
-  }
-  __device__ __forceinline__ bool slow(uint64_t* bar, uint32_t parity) const {
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if (*reinterpret_cast<volatile int*>(abort) != 0) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
-        flag_error(err, KVQ_DEVERR_TIMEOUT);
-        *reinterpret_cast<volatile int*>(abort) = 1;
-        return false;
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+      const uint32_t t0 = timer();
+      while (!(ok = mbar_try_wait(bar, parity))) {
+        if (timer() - t0 > static_cast<uint32_t>(kWaitLimitNs))
+          *reinterpret_cast<volatile int*>(abort) = 1;
+        if (*reinterpret_cast<volatile int*>(abort) != 0) break;
       }
     }
+    return __all_sync(0xffffffffu, ok) != 0;
+  }
+  static __device__ __forceinline__ uint32_t timer() {  // nanoseconds, mod 2^32
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
   }
 };
 
@@ -259,6 +256,13 @@ __device__ __forceinline__ void scan_rows(const ChunkArgs& a, int* pref, Shared*
   __syncthreads();
 }
 
+// A loop count that the compiler does not see through: loops that are to stay
+// rolled were unrolled where it was a constant, pragma or not.
+__device__ __forceinline__ int rolled(int n) {
+  asm volatile("" : "+r"(n));
+  return n;
+}
+
 // ---------------------------------------------------------------- unpacking
 // binary16 pair of the codes at bits S (low half) and 16 + S (high half) of
 // w, S + B <= 8: the code's bits dropped into the mantissa of 2^(10 - S) (whose
@@ -289,22 +293,32 @@ __device__ __forceinline__ __half2 code_field(uint32_t w, int e) {
   }
 }
 
-// A group's (scale, zero) with the largest code's value inside binary16: the
-// stored roundings can push it past 65504 (by 2^-10 of its range at most);
-// the scale then gives up as many last places.
-template <int B>
-__device__ __forceinline__ uint32_t fit_params(uint32_t par) {
-  const float2 f = unpack_half2(par);
-  const float top = static_cast<float>((1 << B) - 1);
-  if (fmaf(top, f.x, f.y) > 65504.0f) {
+// The stored roundings of a group's scale and zero can push its largest value
+// past binary16's range (65504); its scale then gives up last places, four at
+// most (2^-8 of a range of 131008 at most, where the roundings are 2^-10).
+template <int B, int N>
+__device__ __forceinline__ void fit_range(uint32_t (&scale2)[N], const uint32_t (&zero2)[N]) {
+  const __half2 top = __float2half2_rn(static_cast<float>((1 << B) - 1));
+  auto largest = [&](int i) {
+    return __hfma2(top, *reinterpret_cast<const __half2*>(&scale2[i]),
+                   *reinterpret_cast<const __half2*>(&zero2[i]));
+  };
+  __half2 most = largest(0);
+#pragma unroll
+  for (int i = 1; i < N; ++i) most = __hmax2(most, largest(i));
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&most);
+  if ((u & 0xffffu) == 0x7c00u || (u >> 16) == 0x7c00u) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
 #pragma unroll 1
-    for (int i = 0; i < 4 && (par & 0xffffu) != 0; ++i) {
-      par -= 1;  // the next binary16 scale towards zero
-      const float2 g = unpack_half2(par);
-      if (fmaf(top, g.x, g.y) <= 65504.0f) break;
+      for (int k = 0, kn = rolled(4); k < kn; ++k) {
+        const __half2 t = largest(i);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&t);
+        // the next binary16 scale towards zero
+        scale2[i] -= ((w & 0xffffu) == 0x7c00u ? 1u : 0u) + ((w >> 16) == 0x7c00u ? 0x10000u : 0u);
+      }
     }
   }
-  return par;
 }
 
 // hi and lo binary16 pairs of code * scale + zero, for two codes.
@@ -345,42 +359,54 @@ __device__ __forceinline__ void store_chunk(uint8_t* p, const uint32_t (&x)[4]) 
 // of the tile), elements [half * D / HALVES, + D / HALVES).
 template <class C, int B>
 __device__ __forceinline__ void unpack_keys(const uint8_t* codes, const uint32_t* params,
-                                            int group, int pos, int half, bool live,
+                                            int gshift, int pos, int half, bool live,
                                             uint8_t* tile, int r) {
   constexpr int D = C::D, CU = D / 8 / C::HALVES, E = 16 / B;
   constexpr int WORDS = CU >= E ? CU / E : 1;       // words of a slice this lane takes
   constexpr int EW = CU >= E ? E : CU;              // units of a word it takes
   constexpr int LOAD = WORDS < 4 ? WORDS : 4;       // words of one load
-  const int groups = D / group;
+  const int groups = D >> gshift, inside = (1 << gshift) - 32;  // 32-element part in a group
   const uint8_t* row = codes + pos * (D * B / 8) + half * (WORDS * 4) * (CU >= E ? 1 : 0);
   const int pre = CU >= E ? 0 : half * CU * B;      // first unit's field in the word
-  uint32_t scale2 = 0, zero2 = 0;
-#pragma unroll
-  for (int l = 0; l < WORDS / LOAD; ++l) {
+  uint32_t scale2[1] = {0}, zero2[1] = {0};
+  // (rolled over the words: the roles' loops share the instruction caches,
+  // and unrolled ones ran at a fifth of this speed)
+#pragma unroll 1
+  for (int l = 0, ln = rolled(WORDS / LOAD); l < ln; ++l) {
     uint32_t w[4][LOAD];
 #pragma unroll
     for (int c = 0; c < 4; ++c) load_words<LOAD>(row + c * (D * B / 32) + l * 16, w[c]);
-#pragma unroll
-    for (int i = 0; i < LOAD; ++i) {
+#pragma unroll 1
+    for (int i = 0, in = rolled(LOAD); i < in; ++i) {
+      const int u0 = half * CU + (l * LOAD + i) * E;  // first unit of the word
+      // its 16-byte place in the row (units are chunks); unit u0 + e differs in
+      // the bits of e alone
+      uint8_t* dst0 = tile + (u0 / 8) * (C::NT * 128) + r * 128;
+      const int x0 = ((u0 & 7) ^ (r & 7)) << 4;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (CU < E) w[c][i] >>= pre;
+        if (CU < E) w[c][0] >>= pre;
 #pragma unroll
       for (int e = 0; e < EW; ++e) {
-        const int uu = (l * LOAD + i) * E + e, u = half * CU + uu;
-        if (uu % 4 == 0 && (uu == 0 || ((8 * u) & (group - 1)) == 0)) {  // a group begins
-          uint32_t par = live ? fit_params<B>(params[pos * groups + 8 * u / group]) : 0u;
-          scale2 = __byte_perm(par, 0, 0x1010);
-          zero2 = __byte_perm(par, 0, 0x3232);
+        const int u = u0 + e;
+        if (e % 4 == 0 && ((8 * u) & inside) == 0) {  // a group begins
+          const uint32_t par = live ? params[pos * groups + (8 * u >> gshift)] : 0u;
+          scale2[0] = __byte_perm(par, 0, 0x1010);
+          zero2[0] = __byte_perm(par, 0, 0x3232);
+          fit_range<B>(scale2, zero2);
         }
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          value_pair<C::KP>(code_field<B>(w[c][i], e), scale2, zero2, hi[c], lo[c]);
-        uint8_t* dst = tile + (u / 8) * (C::NT * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+          value_pair<C::KP>(code_field<B>(w[c][0], e), scale2[0], zero2[0], hi[c], lo[c]);
+        uint8_t* dst = dst0 + (x0 ^ (e << 4));
         store_chunk(dst, hi);
         if constexpr (C::KP == 2) store_chunk(dst + C::KPIECE, lo);
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int x = 0; x + 1 < LOAD; ++x) w[c][x] = w[c][x + 1];
     }
   }
 }
@@ -390,7 +416,7 @@ __device__ __forceinline__ void unpack_keys(const uint8_t* codes, const uint32_t
 // of the octet's eight positions, u in [half * D/8 / HALVES, ...).
 template <class C, int B>
 __device__ __forceinline__ void unpack_values(const uint8_t* codes, const uint32_t* params,
-                                              int group, int lane, int half, int live,
+                                              int gshift, int lane, int half, int live,
                                               uint8_t* tile, int octet0) {
   constexpr int D = C::D, CU = D / 8 / C::HALVES, E = 16 / B;
   constexpr int W = D * B / 128;                    // words of an octet in a format lane
@@ -398,48 +424,54 @@ __device__ __forceinline__ void unpack_values(const uint8_t* codes, const uint32
   constexpr int WORDS = CU >= E ? CU / E : 1;
   constexpr int EW = CU >= E ? E : CU;
   constexpr int LOAD = WORDS < 4 ? WORDS : 4;
-  const int groups = D / group;
+  const int groups = D >> gshift, inside = (1 << gshift) - 32;
   const int octet = lane >> 3, m = lane & 7;        // octet of the block: 0 .. 3
   const uint8_t* base = codes + (octet >> 1) * (2 * D * B) + 4 * m * P;
   const int q0 = (octet & 1) * W + (CU >= E ? half * WORDS : 0);  // first word
   const int pre = CU >= E ? 0 : half * CU * B;
   const int og = octet0 + octet;                    // octet of the tile
   uint8_t* col = tile + (og >> 3) * (D * 128) + m * 128 + (((og & 7) ^ m) << 4);
-  uint32_t scale2[4], zero2[4];
-#pragma unroll
-  for (int l = 0; l < WORDS / LOAD; ++l) {
+  uint32_t scale2[4] = {0, 0, 0, 0}, zero2[4] = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int l = 0, ln = rolled(WORDS / LOAD); l < ln; ++l) {
     uint32_t w[4][LOAD];
     const int n = 4 * (q0 + l * LOAD);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       load_words<LOAD>(base + (n / P) * (32 * P) + i * P + n % P, w[i]);
-#pragma unroll
-    for (int x = 0; x < LOAD; ++x) {
+#pragma unroll 1
+    for (int x = 0, xn = rolled(LOAD); x < xn; ++x) {
+      const int u0 = half * CU + (l * LOAD + x) * E;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (CU < E) w[i][x] >>= pre;
+        if (CU < E) w[i][0] >>= pre;
 #pragma unroll
       for (int e = 0; e < EW; ++e) {
-        const int uu = (l * LOAD + x) * E + e, u = half * CU + uu;
-        if (uu % 4 == 0 && (uu == 0 || ((8 * u) & (group - 1)) == 0)) {
-          const uint32_t* src = params + (octet * 8) * groups + 8 * u / group;
+        const int u = u0 + e;
+        if (e % 4 == 0 && ((8 * u) & inside) == 0) {
+          const uint32_t* src = params + (octet * 8) * groups + (8 * u >> gshift);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int k = octet * 8 + 2 * i;
-            const uint32_t p0 = k < live ? fit_params<B>(src[(2 * i) * groups]) : 0u;
-            const uint32_t p1 = k + 1 < live ? fit_params<B>(src[(2 * i + 1) * groups]) : 0u;
+            const uint32_t p0 = k < live ? src[(2 * i) * groups] : 0u;
+            const uint32_t p1 = k + 1 < live ? src[(2 * i + 1) * groups] : 0u;
             scale2[i] = __byte_perm(p0, p1, 0x5410);
             zero2[i] = __byte_perm(p0, p1, 0x7632);
           }
+          fit_range<B>(scale2, zero2);
         }
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          value_pair<C::KP>(code_field<B>(w[i][x], e), scale2[i], zero2[i], hi[i], lo[i]);
+          value_pair<C::KP>(code_field<B>(w[i][0], e), scale2[i], zero2[i], hi[i], lo[i]);
         uint8_t* dst = col + u * (8 * 128);
         store_chunk(dst, hi);
         if constexpr (C::KP == 2) store_chunk(dst + C::KPIECE, lo);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int y = 0; y + 1 < LOAD; ++y) w[i][y] = w[i][y + 1];
     }
   }
 }
@@ -449,8 +481,8 @@ template <class C, bool KEYS>
 __device__ __forceinline__ void zero_block(int lane, int half, uint8_t* tile, int blk) {
   constexpr int CU = C::D / 8 / C::HALVES;
   const uint32_t z[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int uu = 0; uu < CU; ++uu) {
+#pragma unroll 1
+  for (int uu = 0, uun = rolled(CU); uu < uun; ++uu) {
     const int u = half * CU + uu;
     uint8_t* dst;
     if (KEYS) {
@@ -476,9 +508,10 @@ __device__ __forceinline__ RingLayout ring_layout(const BlockCache& c, int avail
   l.k = 0;
   l.v = kBlock * c.head_dim * c.bits_k / 8;
   l.kp = l.v + kBlock * c.head_dim * c.bits_v / 8;
-  l.vp = l.kp + kBlock * (c.head_dim / c.group) * 4;
-  l.bytes = l.vp + kBlock * (c.head_dim / c.group_v) * 4;
-  l.blocks = min(kRing, avail / l.bytes);
+  l.vp = l.kp + kBlock * (c.head_dim >> c.gshift_k) * 4;
+  l.bytes = l.vp + kBlock * (c.head_dim >> c.gshift_v) * 4;
+  l.blocks = 0;
+  while (l.blocks < kRing && (l.blocks + 1) * l.bytes <= avail) ++l.blocks;
   return l;
 }
 
@@ -581,7 +614,7 @@ __device__ __forceinline__ bool load_role(const ChunkArgs& a, Shared* sh, uint8_
                 (static_cast<size_t>(block) * a.c.kv_heads + h) * a.c.block_tokens + local;
             uint8_t* dst = ring + slot * rl.bytes;
             const int kb = a.c.head_dim * a.c.bits_k / 8, vb = a.c.head_dim * a.c.bits_v / 8;
-            const int gk = a.c.head_dim / a.c.group, gv = a.c.head_dim / a.c.group_v;
+            const int gk = a.c.head_dim >> a.c.gshift_k, gv = a.c.head_dim >> a.c.gshift_v;
             mbar_arrive_expect_tx(bar, cnt * (kb + vb + 4 * gk + 4 * gv));
             bulk_copy_g2s(dst + rl.k, a.c.k_codes + row * kb, cnt * kb, bar);
             bulk_copy_g2s(dst + rl.kp, a.c.k_params + row * gk, cnt * gk * 4, bar);
@@ -656,7 +689,7 @@ __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint
   const int blk = w / C::HALVES, half = w % C::HALVES;
   uint64_t* full = KEYS ? sh->k_full : sh->v_full;
   uint64_t* empty = KEYS ? sh->k_empty : sh->v_empty;
-  const int group = KEYS ? a.c.group : a.c.group_v;
+  const int gshift = KEYS ? a.c.gshift_k : a.c.gshift_v;
   int slot = 0, tile = 0;
   uint32_t phase = 0;
   for (int piece = 0;; ++piece) {
@@ -687,10 +720,10 @@ __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint
         const uint8_t* src = ring + s * rl.bytes;
         const int live = lim - t * C::NT - blk * kBlock;  // positions of the block that are seen
         if constexpr (KEYS)
-          unpack_keys<C, B>(src + rl.k, reinterpret_cast<const uint32_t*>(src + rl.kp), group,
+          unpack_keys<C, B>(src + rl.k, reinterpret_cast<const uint32_t*>(src + rl.kp), gshift,
                             lane, half, lane < live, dst, blk * kBlock + lane);
         else
-          unpack_values<C, B>(src + rl.v, reinterpret_cast<const uint32_t*>(src + rl.vp), group,
+          unpack_values<C, B>(src + rl.v, reinterpret_cast<const uint32_t*>(src + rl.vp), gshift,
                               lane, half, live, dst, blk * 4);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ring_empty[s]);
@@ -709,20 +742,26 @@ __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint
   }
 }
 
-// MMA issue (warp 16, one lane).
+// MMA issue (warp 16; operands are uniform over the warp, one lane issues).
 template <class C>
 __device__ __forceinline__ void issue_scores(uint32_t s_tmem, uint32_t q, uint32_t k) {
   constexpr uint32_t idesc = tc::idesc_f16_kk(128, C::NT);
+  const uint64_t q0 = tc::smem_desc_k128(q), k0 = tc::smem_desc_k128(k);
+  bool accumulate = false;
   // (Q piece, K piece) products; small ones first
-  constexpr int terms = C::PIECES;
+#pragma unroll 1
+  for (int x = C::PIECES - 1; x >= 0; --x) {
+    uint64_t qa = q0 + (x == 2 ? C::QTILE >> 4 : 0), ka = k0 + (x == 1 ? C::KPIECE >> 4 : 0);
+#pragma unroll 1
+    for (int i = 0, in = rolled(C::D / 64); i < in; ++i) {  // 64 elements: four steps of 16 in a swizzled row
 #pragma unroll
-  for (int x = terms - 1; x >= 0; --x) {
-    const uint32_t qa = q + (x == 2 ? C::QTILE : 0), ka = k + (x == 1 ? C::KPIECE : 0);
-#pragma unroll
-    for (int i = 0; i < C::D / 16; ++i)
-      tc::mma_f16_ss(s_tmem, tc::smem_desc_k128(qa + (i / 4) * (128 * 128) + (i % 4) * 32),
-                     tc::smem_desc_k128(ka + (i / 4) * (C::NT * 128) + (i % 4) * 32), idesc,
-                     !(x == terms - 1 && i == 0));
+      for (int y = 0; y < 4; ++y) {
+        tc::mma_f16_ss(s_tmem, qa + 2 * y, ka + 2 * y, idesc, accumulate);
+        accumulate = true;
+      }
+      qa += (128 * 128) >> 4;
+      ka += (C::NT * 128) >> 4;
+    }
   }
 }
 
@@ -730,75 +769,86 @@ template <class C>
 __device__ __forceinline__ void issue_output(uint32_t o_tmem, uint32_t p_tmem, uint32_t v,
                                              bool accumulate) {
   constexpr uint32_t idesc = tc::idesc_f16_kk(128, C::D);
-  constexpr int terms = C::PIECES;
+  const uint64_t v0 = tc::smem_desc_k128(v);
+#pragma unroll 1
+  for (int x = C::PIECES - 1; x >= 0; --x) {
+    uint32_t pa = p_tmem + (x == 2 ? C::NT / 2 : 0);
+    uint64_t va = v0 + (x == 1 ? C::KPIECE >> 4 : 0);
+#pragma unroll 1
+    for (int i = 0, in = rolled(C::NT / 64); i < in; ++i) {
 #pragma unroll
-  for (int x = terms - 1; x >= 0; --x) {
-    const uint32_t pa = p_tmem + (x == 2 ? C::NT / 2 : 0), va = v + (x == 1 ? C::KPIECE : 0);
-#pragma unroll
-    for (int i = 0; i < C::NT / 16; ++i)
-      tc::mma_f16_ts(o_tmem, pa + i * 8,
-                     tc::smem_desc_k128(va + (i / 4) * (C::D * 128) + (i % 4) * 32), idesc,
-                     accumulate || !(x == terms - 1 && i == 0));
+      for (int y = 0; y < 4; ++y) {
+        tc::mma_f16_ts(o_tmem, pa + 8 * y, va + 2 * y, idesc, accumulate);
+        accumulate = true;
+      }
+      pa += 32;
+      va += (C::D * 128) >> 4;
+    }
   }
 }
 
 template <class C>
 __device__ __forceinline__ bool mma_role(Shared* sh, uint32_t smem, uint32_t tmem,
                                          const Waiter& wait) {
-  int tile0 = 0;                      // tiles of the pieces before
-  uint32_t p_phase[2] = {0, 0};
+  int tile0 = 0;  // tiles of the pieces before
+  uint32_t p_phase = 0;  // bit s: slot s
   for (int piece = 0;; ++piece) {
-    if (!wait.one(&sh->d_full[piece & 1], (piece >> 1) & 1)) return false;
-    const Piece p = sh->piece[piece & 1];
-    if (!p.valid) return true;
-    mbar_arrive(&sh->d_empty[piece & 1]);
-    // slot s works in step j iff active(s, j); on tile tile_of(s, j)
-    auto active = [&](int s, int j) {
-      return j < p.j1 && (p.wide ? (s == 1 ? j < p.t1 : j < p.nt0) : 2 * j + s < p.t1);
-    };
-    auto index = [&](int s, int j) { return tile0 + (p.wide ? j : 2 * j + s) - p.t0; };
-    // queries are needed before the first scores, a K tile by its first user
-    if (!wait.one(&sh->q_full, piece & 1)) return false;
-    int k_seen = tile0;               // K tiles waited for
-    auto scores = [&](int s, int j) {
-      const int t = index(s, j);
-      if (t == k_seen) {
-        if (!wait.one(&sh->k_full[t & 1], (t >> 1) & 1)) return false;
-        ++k_seen;
-      }
-      tc::fence_after_sync();
-      const uint32_t q = smem + (p.wide && s == 1 ? C::QTILE : 0);
-      issue_scores<C>(tmem + s * C::S_COL, q, smem + C::SMEM_K + (t & 1) * C::STAGE);
-      tc::commit(&sh->s_full[s]);
-      if (!p.wide || s == 1) tc::commit(&sh->k_empty[t & 1]);
-      return true;
-    };
-    for (int s = 0; s < 2; ++s)
-      if (active(s, p.j0) && !scores(s, p.j0)) return false;
-    int v_seen = tile0;
-    for (int j = p.j0; j < p.j1; ++j) {
+    if (!wait(&sh->d_full[piece & 1], (piece >> 1) & 1)) return false;
+    const Piece& pd = sh->piece[piece & 1];
+    if (!pd.valid) return true;
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const bool wide = uniform(pd.wide) != 0;
+    const int t0 = uniform(pd.t0), t1 = uniform(pd.t1), j0 = uniform(pd.j0), j1 = uniform(pd.j1);
+    const int nt0 = uniform(pd.nt0);
+    if (tc::elect_one()) mbar_arrive(&sh->d_empty[piece & 1]);
+    if (!wait(&sh->q_full, piece & 1)) return false;
+    // The scores of a slot's next tile follow the output product of its last
+    // one; step j0 - 1 stands for the start, where only scores are issued.
+    int k_seen = t0, v_seen = t0;  // tiles waited for
 #pragma unroll 1
-      for (int s = 0; s < 2; ++s) {
-        if (!active(s, j)) continue;
-        const int t = index(s, j);
-        if (!wait.one(&sh->p_full[s], p_phase[s])) return false;
-        p_phase[s] ^= 1;
-        if (t == v_seen) {
-          if (!wait.one(&sh->v_full[t & 1], (t >> 1) & 1)) return false;
-          ++v_seen;
+    for (int j = j0 - 1; j < j1; ++j) {
+#pragma unroll 1
+      for (int s = 0, sn = rolled(2); s < sn; ++s) {
+        // slot s works in step j on tile t, in step j + 1 on tile u
+        const int t = wide ? j : 2 * j + s, u = wide ? j + 1 : t + 2;
+        const int tend = wide && s == 0 ? min(t1, nt0) : t1;
+        const uint32_t s_tmem = tmem + s * C::S_COL;
+        const bool output = j >= j0 && t < tend;
+        if (output) {
+          if (!wait(&sh->p_full[s], (p_phase >> s) & 1)) return false;
+          p_phase ^= 1u << s;
+          const int i = tile0 + t - t0;
+          if (t == v_seen) {
+            if (!wait(&sh->v_full[i & 1], (i >> 1) & 1)) return false;
+            ++v_seen;
+          }
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            issue_output<C>(tmem + C::O_BASE + s * C::O_COL, s_tmem,
+                            smem + C::SMEM_V + (i & 1) * C::STAGE, j > j0);
+            if (!wide || s == 1) tc::commit(&sh->v_empty[i & 1]);
+          }
         }
-        tc::fence_after_sync();
-        issue_output<C>(tmem + C::O_BASE + s * C::O_COL, tmem + s * C::S_COL,
-                        smem + C::SMEM_V + (t & 1) * C::STAGE, j > p.j0);
-        if (!p.wide || s == 1) tc::commit(&sh->v_empty[t & 1]);
-        if (active(s, j + 1)) {
-          if (!scores(s, j + 1)) return false;
-        } else {
-          tc::commit(&sh->s_full[s]);  // the slot's output is complete
+        if (j + 1 < j1 && u < tend) {
+          const int i = tile0 + u - t0;
+          if (u == k_seen) {
+            if (!wait(&sh->k_full[i & 1], (i >> 1) & 1)) return false;
+            ++k_seen;
+          }
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            issue_scores<C>(s_tmem, smem + (wide && s == 1 ? C::QTILE : 0),
+                            smem + C::SMEM_K + (i & 1) * C::STAGE);
+            tc::commit(&sh->s_full[s]);
+            if (!wide || s == 1) tc::commit(&sh->k_empty[i & 1]);
+          }
+        } else if (output) {
+          if (tc::elect_one()) tc::commit(&sh->s_full[s]);  // the slot's output is complete
         }
+        __syncwarp();
       }
     }
-    tile0 += p.t1 - p.t0;
+    tile0 += t1 - t0;
   }
 }
 
@@ -903,6 +953,40 @@ __device__ __forceinline__ void store_out8(void* out, int dtype, size_t i, const
   }
 }
 
+// Two binary32 values side by side (packed operations of sm_100).
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// Weights 2^(s c + shift) of two scores, rounded to binary16 (p; q: the rest of
+// the rounding, for three pieces), and their sums in binary32 (sum2).
+template <int PIECES>
+__device__ __forceinline__ void weights(uint32_t u, uint32_t v, uint64_t c2, uint64_t shift2,
+                                        uint64_t& sum2, uint32_t& p, uint32_t& q) {
+  uint64_t s;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(s)
+      : "l"(pair(__uint_as_float(u), __uint_as_float(v))), "l"(c2), "l"(shift2));
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(s));
+  x = exp2_approx(x);
+  y = exp2_approx(y);
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum2) : "l"(pair(x, y)));
+  p = f2_to_h2(x, y);
+  if constexpr (PIECES == 3) {
+    const float2 h = unpack_half2(p);
+    q = f2_to_h2(x - h.x, y - h.y);
+  }
+}
+
+__device__ __forceinline__ float sum_of(uint64_t s) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(s));
+  return x + y;
+}
+
 // Softmax of one slot (warps 0-3: slot 0, 4-7: slot 1).
 template <class C, bool ROT>
 __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uint8_t* smem,
@@ -962,82 +1046,103 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       s_phase ^= 1;
       tc::fence_after_sync();
       if (works) {
-        // the scores are read twice, 32 columns at a time, for their maximum
-        // and for the weights: held in registers (NT of them) they spill
+        // The scores are read twice, for their maximum and for the weights.
+        // (One pass with the weights held in registers until the maximum is
+        // known was slower: its loop, unrolled over the registers, does not
+        // stay in the instruction cache beside the other roles'.)
         const int seen = limit - t * NT;
-        const bool masks = __any_sync(0xffffffffu, seen < NT);
-        float mx = -INFINITY;
+        if (__any_sync(0xffffffffu, seen < NT)) {  // masked: -inf in place
+#pragma unroll 1
+          for (int i = 0, in = rolled(NT / 16); i < in; ++i) {
+            uint32_t s[16];
+            tc::ld_32x32b<16>(s_tmem + 16 * i, s);
+            tc::wait_ld(s);
 #pragma unroll
-        for (int i = 0; i < NT / 32; ++i) {
-          uint32_t s[32];
-          tc::ld_32x32b<32>(s_tmem + 32 * i, s);
-          tc::wait_ld(s);
-          if (masks) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (32 * i + k >= seen) s[k] = 0xff800000u;  // -inf
+            for (int k = 0; k < 16; ++k)
+              if (16 * i + k >= seen) s[k] = 0xff800000u;
+            tc::st_32x32b_x16(s_tmem + 16 * i, s);
           }
-#pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
+          tc::wait_st();
         }
-        mx = fmaxf(mx, m);
-        const bool grown = (mx - m) * c > C::kThreshold;  // (false while nothing is seen)
+        float mx = m;
+        {
+          uint32_t s[2][16];  // 16 scores at a time, the next ones on their way
+          tc::ld_32x32b<16>(s_tmem, s[0]);
+#pragma unroll 1
+          for (int i = 0, in = rolled(NT / 32); i < in; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              tc::wait_ld(s[x]);
+              // (the last read wraps round)
+              tc::ld_32x32b<16>(s_tmem + ((32 * i + 16 * x + 16) & (NT - 1)), s[x ^ 1]);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(s[x][k]));
+            }
+          }
+          tc::wait_ld(s[0]);
+        }
         if (first) {
           m = mx;
-        } else if (__any_sync(0xffffffffu, grown)) {
-          // every row moves to its maximum; its sums follow
+        } else if (__any_sync(0xffffffffu, (mx - m) * c > C::kThreshold)) {
+          // (false while nothing is seen) every row moves to its maximum, and
+          // its sums follow
           const float f = mx == -INFINITY ? 1.0f : exp2_approx((m - mx) * c);
           l *= f;
           m = mx;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tc::ld_32x32b<32>(o_tmem + 32 * i, o);
+#pragma unroll 1
+          for (int i = 0, in = rolled(D / 16); i < in; ++i) {
+            uint32_t o[16];
+            tc::ld_32x32b<16>(o_tmem + 16 * i, o);
             tc::wait_ld(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tc::st_32x32b_x32(o_tmem + 32 * i, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tc::st_32x32b_x16(o_tmem + 16 * i, o);
           }
         }
         const float shift = C::kOffset - (m == -INFINITY ? 0.0f : m * c);
-        float l0 = 0.0f, l1 = 0.0f;
-        // (two binary16 pieces take a score's column each: all scores are read
-        // before the first are written; one piece's columns trail the reads)
-        constexpr int HELD = C::PIECES == 3 ? NT : 32;
+        const uint64_t c2 = pair(c, c), shift2 = pair(shift, shift);
+        uint64_t sum2 = 0;
+        if constexpr (C::PIECES < 3) {
+          uint32_t s[2][16];  // (a chunk's weights take columns that were read)
+          tc::ld_32x32b<16>(s_tmem, s[0]);
+#pragma unroll 1
+          for (int i = 0, in = rolled(NT / 32); i < in; ++i) {
+            uint32_t p[16];
 #pragma unroll
-        for (int h = 0; h < NT / HELD; ++h) {
-          uint32_t s[HELD];
+            for (int x = 0; x < 2; ++x) {
+              tc::wait_ld(s[x]);
+              if (x == 0 || i + 1 < NT / 32)
+                tc::ld_32x32b<16>(s_tmem + 32 * i + 16 * x + 16, s[x ^ 1]);
 #pragma unroll
-          for (int i = 0; i < HELD / 32; ++i)
-            tc::ld_32x32b<32>(s_tmem + HELD * h + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
-#pragma unroll
-          for (int i = 0; i < HELD / 32; ++i)
-            tc::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
-          if (masks) {
-#pragma unroll
-            for (int k = 0; k < HELD; ++k)
-              if (HELD * h + k >= seen) s[k] = 0xff800000u;
-          }
-#pragma unroll
-          for (int i = 0; i < HELD / 32; ++i) {
-            uint32_t p[16], q[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float x = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k]), c, shift));
-              const float y = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k + 1]), c, shift));
-              l0 += x;
-              l1 += y;
-              p[k] = f2_to_h2(x, y);
-              if constexpr (C::PIECES == 3) {
-                const float2 hh = unpack_half2(p[k]);
-                q[k] = f2_to_h2(x - hh.x, y - hh.y);
+              for (int k = 0; k < 8; ++k) {
+                uint32_t none;
+                weights<C::PIECES>(s[x][2 * k], s[x][2 * k + 1], c2, shift2, sum2, p[8 * x + k],
+                                   none);
               }
             }
-            tc::st_32x32b_x16(s_tmem + HELD / 2 * h + 16 * i, p);
-            if constexpr (C::PIECES == 3) tc::st_32x32b_x16(s_tmem + NT / 2 + 16 * i, q);
+            tc::st_32x32b_x16(s_tmem + 16 * i, p);
+          }
+        } else {
+          // two binary16 pieces take a score's column each: all scores are
+          // read before the first are written
+          uint32_t s[NT];
+#pragma unroll
+          for (int i = 0; i < NT / 32; ++i)
+            tc::ld_32x32b<32>(s_tmem + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+#pragma unroll
+          for (int i = 0; i < NT / 32; ++i)
+            tc::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+#pragma unroll
+          for (int i = 0; i < NT / 32; ++i) {
+            uint32_t p[16], q[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              weights<3>(s[32 * i + 2 * k], s[32 * i + 2 * k + 1], c2, shift2, sum2, p[k], q[k]);
+            tc::st_32x32b_x16(s_tmem + 16 * i, p);
+            tc::st_32x32b_x16(s_tmem + NT / 2 + 16 * i, q);
           }
         }
-        l += l0 + l1;
+        l += sum_of(sum2);
         tc::wait_st();
       }
       tc::fence_before_sync();
@@ -1093,8 +1198,8 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
         if (valid) a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, l);
       }
       const size_t orow = (static_cast<size_t>(token) * a.q_heads + head) * D;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+#pragma unroll 1
+      for (int i = 0, in = rolled(D / 32); i < in; ++i) {
         uint32_t o[32];
         if (any_tile) {
           tc::ld_32x32b<32>(o_tmem + 32 * i, o);
@@ -1143,9 +1248,9 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
 
 template <class C, bool ROT>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
-  extern __shared__ uint8_t raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (the swizzled tiles want 1024-byte boundaries; a pointer rounded up here
+  // would lose its address space, and every access become a generic one)
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + C::SMEM_RING;
   Shared* sh = reinterpret_cast<Shared*>(smem + kSmemMax - kHeader);
   const RingLayout rl = ring_layout(a.c, kSmemMax - kHeader - C::SMEM_RING);
@@ -1183,7 +1288,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh->tmem;
-  const Waiter wait{a.err, &sh->abort};
+  const Waiter wait{&sh->abort};
 
   if (warp < kWarpsK) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -1210,8 +1315,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kWarpMma) {
-      if ((threadIdx.x & 31) == 0) mma_role<C>(sh, smem_addr(smem), tmem, wait);
-      __syncwarp();
+      mma_role<C>(sh, smem_addr(smem), __shfl_sync(0xffffffffu, tmem, 0), wait);
     } else if (warp == kWarpLoad) {
       load_role<C>(a, sh, ring, rl, pref, wait);
     }
@@ -1220,7 +1324,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
   __syncthreads();
   if (warp == kWarpMma) {
     tc::fence_after_sync();
-    if (sh->abort != 0) {  // (products in flight end before their memory is given back)
+    if (sh->abort != 0) {
+      if ((threadIdx.x & 31) == 0) flag_error(a.err, KVQ_DEVERR_TIMEOUT);
+      // products in flight end before their memory is given back
       if ((threadIdx.x & 31) == 0) {
         mbar_init(&sh->q_full, 1);
         fence_barrier_init();

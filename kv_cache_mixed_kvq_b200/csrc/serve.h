@@ -35,6 +35,7 @@ struct BlockCache {
   uint32_t* k_params;
   uint32_t* v_params;
   int kv_heads, head_dim, bits_k, bits_v, group, group_v;
+  int gshift_k, gshift_v;  // log2 of the group sizes
   int blocks;        // pages, or batch rows
   int block_tokens;  // positions of a block
   bool rotate_keys;
