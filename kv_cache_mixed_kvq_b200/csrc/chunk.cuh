@@ -31,10 +31,10 @@
 //   warps 12-15 values: the same to a V tile (rows are elements: K-major along
 //               the positions, which is the order of the packed V tiles)
 //   warp 16     issues the MMAs
-//   warp 17     walks the work list, publishes each piece of work, and copies
-//               the packed codes and parameters of 32 positions at a time into
-//               the ring (cp.async.bulk)
-//   warps 18-19 idle (registers are split by groups of four warps)
+//   warp 17     walks the work list and publishes each piece of work
+//   warps 18-19 copy packed codes and parameters, 32 positions at a time, into
+//               the ring (cp.async: four bulk copies a block, each set up in
+//               uniform registers, took 900 cycles of the one warp)
 // In a wide unit (more than 128 rows) the slots are its two halves and share
 // each K and V tile; in a narrow one they take alternate tiles of the same
 // rows and are merged at the end, so that one slot's softmax runs while the
@@ -62,11 +62,12 @@ namespace kvq {
 namespace chunk {
 
 constexpr int kThreads = 20 * 32;
-constexpr int kWarpsK = 8, kWarpsV = 12, kWarpMma = 16, kWarpLoad = 17;
+constexpr int kWarpsK = 8, kWarpsV = 12, kWarpMma = 16, kWarpList = 17, kWarpCopy = 18;
+constexpr int kCopiers = 2;       // warps that copy, block by block in turn
 // Registers a thread at launch, and of each warpgroup after the split: the
-// softmax groups take what the others give, 256 x 144 + 256 x 64 + 128 x 64
+// softmax groups take what the others give, 256 x 128 + 256 x 80 + 128 x 64
 // = 640 x 96.  (Five warps share an SM quarter's 16384 registers, hence 96.)
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsUnpack = 64, kRegsIssue = 64;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsUnpack = 80, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThreads * kRegsLaunch,
               "more registers than the launch has would never be granted");
 constexpr int kRing = 16;         // ring blocks at most
@@ -80,8 +81,8 @@ struct Cfg {
   static constexpr int NT = NT_;                     // positions of a tile
   static constexpr int KP = PIECES == 1 ? 1 : 2;     // pieces of a key or value
   static constexpr int UNIT = unit_rows(PIECES);     // rows of a unit
-  static constexpr int HALVES = 128 / NT;            // warps that share a ring block
   static constexpr int BLOCKS = NT / kBlock;
+  static constexpr int PARTS = 4 / BLOCKS;           // warps that share a ring block
   static constexpr int QTILE = 128 * D * 2;          // bytes of one Q region
   static constexpr int KPIECE = NT * D * 2;
   static constexpr int STAGE = KPIECE * KP;          // bytes of a K or V tile
@@ -355,135 +356,128 @@ __device__ __forceinline__ void store_chunk(uint8_t* p, const uint32_t (&x)[4]) 
   *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
 }
 
+// Place of a 16-byte chunk of key row r (of a ring block) among the row's
+// D B / 128 chunks: exchanged so that the loads of eight rows' same chunk hit
+// different banks.
+__device__ __forceinline__ int key_chunk_swizzle(int chunks, int r) {
+  return chunks >= 8 ? r & 7 : chunks == 4 ? (r >> 1) & 3 : chunks == 2 ? (r >> 2) & 1 : 0;
+}
+
 // Keys of one ring block into rows of the K tile: one lane a position (row r
-// of the tile), elements [half * D / HALVES, + D / HALVES).
+// of the tile), elements [part * D / PARTS, + D / PARTS).  Straight code: a
+// loop over the words, with its branches and register moves, took half as long
+// again.
 template <class C, int B>
 __device__ __forceinline__ void unpack_keys(const uint8_t* codes, const uint32_t* params,
-                                            int gshift, int pos, int half, bool live,
+                                            int gshift, int pos, int part, bool live,
                                             uint8_t* tile, int r) {
-  constexpr int D = C::D, CU = D / 8 / C::HALVES, E = 16 / B;
-  constexpr int WORDS = CU >= E ? CU / E : 1;       // words of a slice this lane takes
-  constexpr int EW = CU >= E ? E : CU;              // units of a word it takes
-  constexpr int LOAD = WORDS < 4 ? WORDS : 4;       // words of one load
-  const int groups = D >> gshift, inside = (1 << gshift) - 32;  // 32-element part in a group
-  const uint8_t* row = codes + pos * (D * B / 8) + half * (WORDS * 4) * (CU >= E ? 1 : 0);
-  const int pre = CU >= E ? 0 : half * CU * B;      // first unit's field in the word
-  uint32_t scale2[1] = {0}, zero2[1] = {0};
-  // (rolled over the words: the roles' loops share the instruction caches,
-  // and unrolled ones ran at a fifth of this speed)
-#pragma unroll 1
-  for (int l = 0, ln = rolled(WORDS / LOAD); l < ln; ++l) {
+  constexpr int D = C::D, NS = D / 32 / C::PARTS;  // 32-element spans of this lane
+  constexpr int WORDS = NS * B / 4 > 0 ? NS * B / 4 : 1;  // words of a slice it takes
+  constexpr int LOAD = WORDS < 4 ? WORDS : 4;
+  constexpr int E = 16 / B;
+  const int groups = D >> gshift;
+  uint32_t scale2[NS], zero2[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const uint32_t par = live ? params[pos * groups + ((part * NS + i) * 32 >> gshift)] : 0u;
+    scale2[i] = __byte_perm(par, 0, 0x1010);
+    zero2[i] = __byte_perm(par, 0, 0x3232);
+  }
+  fit_range<B>(scale2, zero2);
+  const uint8_t* row = codes + pos * (D * B / 8);
+  const int swz = key_chunk_swizzle(D * B / 128, pos) << 4;
+  const int w0 = part * NS * B / 4;                        // first word of a slice
+  const int pre = B == 2 && NS == 1 ? (part & 1) * 8 : 0;  // half a word is this lane's
+  uint8_t* dst = tile + r * 128;
+  const int rx = (r & 7) << 4;
+#pragma unroll
+  for (int l = 0; l < WORDS / LOAD; ++l) {
     uint32_t w[4][LOAD];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) load_words<LOAD>(row + c * (D * B / 32) + l * 16, w[c]);
-#pragma unroll 1
-    for (int i = 0, in = rolled(LOAD); i < in; ++i) {
-      const int u0 = half * CU + (l * LOAD + i) * E;  // first unit of the word
-      // its 16-byte place in the row (units are chunks); unit u0 + e differs in
-      // the bits of e alone
-      uint8_t* dst0 = tile + (u0 / 8) * (C::NT * 128) + r * 128;
-      const int x0 = ((u0 & 7) ^ (r & 7)) << 4;
+    for (int c = 0; c < 4; ++c) {
+      const int off = c * (D * B / 32) + 4 * (w0 + l * LOAD);
+      load_words<LOAD>(row + (((off & ~15) ^ swz) | (off & 15)), w[c]);
+      if (B == 2 && NS == 1) w[c][0] >>= pre;
+    }
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (CU < E) w[c][0] >>= pre;
+    for (int i = 0; i < LOAD; ++i) {
 #pragma unroll
-      for (int e = 0; e < EW; ++e) {
-        const int u = u0 + e;
-        if (e % 4 == 0 && ((8 * u) & inside) == 0) {  // a group begins
-          const uint32_t par = live ? params[pos * groups + (8 * u >> gshift)] : 0u;
-          scale2[0] = __byte_perm(par, 0, 0x1010);
-          zero2[0] = __byte_perm(par, 0, 0x3232);
-          fit_range<B>(scale2, zero2);
-        }
+      for (int e = 0; e < (NS * 4 < E ? NS * 4 : E); ++e) {
+        const int uu = (l * LOAD + i) * E + e, u = part * NS * 4 + uu;  // unit of the lane, the row
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          value_pair<C::KP>(code_field<B>(w[c][0], e), scale2[0], zero2[0], hi[c], lo[c]);
-        uint8_t* dst = dst0 + (x0 ^ (e << 4));
-        store_chunk(dst, hi);
-        if constexpr (C::KP == 2) store_chunk(dst + C::KPIECE, lo);
+          value_pair<C::KP>(code_field<B>(w[c][i], e), scale2[uu / 4], zero2[uu / 4], hi[c], lo[c]);
+        uint8_t* at = dst + (u / 8) * (C::NT * 128) + (((u & 7) << 4) ^ rx);
+        store_chunk(at, hi);
+        if constexpr (C::KP == 2) store_chunk(at + C::KPIECE, lo);
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int x = 0; x + 1 < LOAD; ++x) w[c][x] = w[c][x + 1];
     }
   }
 }
 
 // Values of one ring block into columns of the V tile (its rows are elements,
 // 64 positions a 128-byte row): lane = 8 octet + m takes the elements 8u + m
-// of the octet's eight positions, u in [half * D/8 / HALVES, ...).
+// of the octet's eight positions, u in [part * D/8 / PARTS, ...).
 template <class C, int B>
 __device__ __forceinline__ void unpack_values(const uint8_t* codes, const uint32_t* params,
-                                              int gshift, int lane, int half, int live,
+                                              int gshift, int lane, int part, int live,
                                               uint8_t* tile, int octet0) {
-  constexpr int D = C::D, CU = D / 8 / C::HALVES, E = 16 / B;
+  constexpr int D = C::D, NS = D / 32 / C::PARTS;
   constexpr int W = D * B / 128;                    // words of an octet in a format lane
   constexpr int N = D * B / 16, P = N < 16 ? N : 16;
-  constexpr int WORDS = CU >= E ? CU / E : 1;
-  constexpr int EW = CU >= E ? E : CU;
-  constexpr int LOAD = WORDS < 4 ? WORDS : 4;
-  const int groups = D >> gshift, inside = (1 << gshift) - 32;
+  constexpr int LOAD = B == 8 ? 2 : 1;              // words of a 32-element span
+  constexpr int E = 16 / B;
+  const int groups = D >> gshift, inside = (1 << gshift) - 32;  // 32-element part in a group
   const int octet = lane >> 3, m = lane & 7;        // octet of the block: 0 .. 3
   const uint8_t* base = codes + (octet >> 1) * (2 * D * B) + 4 * m * P;
-  const int q0 = (octet & 1) * W + (CU >= E ? half * WORDS : 0);  // first word
-  const int pre = CU >= E ? 0 : half * CU * B;
   const int og = octet0 + octet;                    // octet of the tile
   uint8_t* col = tile + (og >> 3) * (D * 128) + m * 128 + (((og & 7) ^ m) << 4);
   uint32_t scale2[4] = {0, 0, 0, 0}, zero2[4] = {0, 0, 0, 0};
 #pragma unroll 1
-  for (int l = 0, ln = rolled(WORDS / LOAD); l < ln; ++l) {
+  for (int i = 0, n = rolled(NS); i < n; ++i) {
+    const int span = part * NS + i;
     uint32_t w[4][LOAD];
-    const int n = 4 * (q0 + l * LOAD);
+    const int nb = 4 * ((octet & 1) * W + span * B / 4);
+    const uint8_t* src = base + (nb / P) * (32 * P) + nb % P;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_words<LOAD>(base + (n / P) * (32 * P) + i * P + n % P, w[i]);
-#pragma unroll 1
-    for (int x = 0, xn = rolled(LOAD); x < xn; ++x) {
-      const int u0 = half * CU + (l * LOAD + x) * E;
+    for (int x = 0; x < 4; ++x) {
+      load_words<LOAD>(src + x * P, w[x]);
+      if (B == 2) w[x][0] >>= (span & 1) * 8;
+    }
+    if (i == 0 || ((32 * span) & inside) == 0) {  // a group begins
+      const uint32_t* par = params + (octet * 8) * groups + (32 * span >> gshift);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (CU < E) w[i][0] >>= pre;
-#pragma unroll
-      for (int e = 0; e < EW; ++e) {
-        const int u = u0 + e;
-        if (e % 4 == 0 && ((8 * u) & inside) == 0) {
-          const uint32_t* src = params + (octet * 8) * groups + (8 * u >> gshift);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = octet * 8 + 2 * i;
-            const uint32_t p0 = k < live ? src[(2 * i) * groups] : 0u;
-            const uint32_t p1 = k + 1 < live ? src[(2 * i + 1) * groups] : 0u;
-            scale2[i] = __byte_perm(p0, p1, 0x5410);
-            zero2[i] = __byte_perm(p0, p1, 0x7632);
-          }
-          fit_range<B>(scale2, zero2);
-        }
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          value_pair<C::KP>(code_field<B>(w[i][0], e), scale2[i], zero2[i], hi[i], lo[i]);
-        uint8_t* dst = col + u * (8 * 128);
-        store_chunk(dst, hi);
-        if constexpr (C::KP == 2) store_chunk(dst + C::KPIECE, lo);
+      for (int x = 0; x < 4; ++x) {
+        const int k = octet * 8 + 2 * x;
+        const uint32_t p0 = k < live ? par[(2 * x) * groups] : 0u;
+        const uint32_t p1 = k + 1 < live ? par[(2 * x + 1) * groups] : 0u;
+        scale2[x] = __byte_perm(p0, p1, 0x5410);
+        zero2[x] = __byte_perm(p0, p1, 0x7632);
       }
+      fit_range<B>(scale2, zero2);
+    }
+    uint8_t* dst = col + span * (4 * 8 * 128);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int e = 0; e < 4; ++e) {
+      uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int y = 0; y + 1 < LOAD; ++y) w[i][y] = w[i][y + 1];
+      for (int x = 0; x < 4; ++x)
+        value_pair<C::KP>(code_field<B>(w[x][e / E], e % E), scale2[x], zero2[x], hi[x], lo[x]);
+      store_chunk(dst + e * (8 * 128), hi);
+      if constexpr (C::KP == 2) store_chunk(dst + e * (8 * 128) + C::KPIECE, lo);
     }
   }
 }
 
 // Positions that no row of the unit sees: zero, so that weights of 0 stay 0.
 template <class C, bool KEYS>
-__device__ __forceinline__ void zero_block(int lane, int half, uint8_t* tile, int blk) {
-  constexpr int CU = C::D / 8 / C::HALVES;
+__device__ __forceinline__ void zero_block(int lane, int part, uint8_t* tile, int blk) {
+  constexpr int CU = C::D / 8 / C::PARTS;
   const uint32_t z[4] = {0, 0, 0, 0};
 #pragma unroll 1
   for (int uu = 0, uun = rolled(CU); uu < uun; ++uu) {
-    const int u = half * CU + uu;
+    const int u = part * CU + uu;
     uint8_t* dst;
     if (KEYS) {
       const int r = blk * kBlock + lane;
@@ -515,10 +509,9 @@ __device__ __forceinline__ RingLayout ring_layout(const BlockCache& c, int avail
   return l;
 }
 
-// Work list and copies (warp 17).
+// Work list (warp 17).
 template <class C>
-__device__ __forceinline__ bool load_role(const ChunkArgs& a, Shared* sh, uint8_t* ring,
-                                          const RingLayout& rl, const int* pref,
+__device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const int* pref,
                                           const Waiter& wait) {
   const int lane = threadIdx.x & 31;
   const int Wu = sh->total;
@@ -527,8 +520,7 @@ __device__ __forceinline__ bool load_role(const ChunkArgs& a, Shared* sh, uint8_
   if (share < a.min_share) share = a.min_share;
   long long w = share * blockIdx.x;
   const long long w1 = min(W, w + share);
-  int piece = 0, slot = 0;
-  uint32_t phase = 0;
+  int piece = 0;
   uint32_t headers = 0;  // partial slots that this CTA filled
   bool ok = true;
   if (w < w1) {
@@ -585,50 +577,6 @@ __device__ __forceinline__ bool load_role(const ChunkArgs& a, Shared* sh, uint8_
         }
       }
       ++piece;
-      // copy its positions, 32 at a time; the pages of 32 blocks looked up at once
-      const int first = t0 * C::NT, last = min(u.lim, t1 * C::NT);
-      int page = 0;
-      for (int p = first, i = 0; p < last; p += kBlock, ++i) {
-        if ((i & 31) == 0) {
-          const int q = p + lane * kBlock;
-          page = b;
-          if (a.table != nullptr && q < last) {
-            page = __ldg(a.table + static_cast<size_t>(b) * a.pages_per_seq + (q >> a.page_shift));
-            if (page < 0 || page >= a.c.blocks) {
-              flag_error(a.err, KVQ_DEVERR_BAD_PAGE);
-              page = -1;
-            }
-          }
-        }
-        const int block = __shfl_sync(0xffffffffu, page, i & 31);
-        ok = wait(&sh->ring_empty[slot], phase ^ 1);
-        if (!ok) break;
-        if (lane == 0) {
-          uint64_t* bar = &sh->ring_full[slot];
-          if (block < 0) {
-            mbar_arrive(bar);  // (that row's output is unspecified)
-          } else {
-            const int local = a.table != nullptr ? p & ((1 << a.page_shift) - 1) : p;
-            const int cnt = min(kBlock, (last - p + 15) & ~15);  // whole V tiles
-            const size_t row =
-                (static_cast<size_t>(block) * a.c.kv_heads + h) * a.c.block_tokens + local;
-            uint8_t* dst = ring + slot * rl.bytes;
-            const int kb = a.c.head_dim * a.c.bits_k / 8, vb = a.c.head_dim * a.c.bits_v / 8;
-            const int gk = a.c.head_dim >> a.c.gshift_k, gv = a.c.head_dim >> a.c.gshift_v;
-            mbar_arrive_expect_tx(bar, cnt * (kb + vb + 4 * gk + 4 * gv));
-            bulk_copy_g2s(dst + rl.k, a.c.k_codes + row * kb, cnt * kb, bar);
-            bulk_copy_g2s(dst + rl.kp, a.c.k_params + row * gk, cnt * gk * 4, bar);
-            bulk_copy_g2s(dst + rl.v, a.c.v_codes + row * vb, cnt * vb, bar);
-            bulk_copy_g2s(dst + rl.vp, a.c.v_params + row * gv, cnt * gv * 4, bar);
-          }
-        }
-        __syncwarp();
-        if (++slot == rl.blocks) {
-          slot = 0;
-          phase ^= 1;
-        }
-      }
-      if (!ok) break;
       w += a.whole_units ? 1 : je - j;
       j = 0;
       if (w < w1 && je == u.steps && ++m == mt) {  // the next row with tokens
@@ -664,20 +612,88 @@ __device__ __forceinline__ bool load_role(const ChunkArgs& a, Shared* sh, uint8_
       if (!(headers & 1u)) a.ws_head[(blockIdx.x * 2 + 0) * 8] = 0;
       if (!(headers & 2u)) a.ws_head[(blockIdx.x * 2 + 1) * 8] = 0;
     }
-    // copies in flight end before the CTA does: a block is refilled only
-    // after it was waited for, so only the last ones can be pending
-    if (!ok) {
-      for (int i = 0; i < rl.blocks; ++i) {
-        const int s = (slot + i) % rl.blocks;
-        const uint32_t ph = s >= slot ? phase ^ 1 : phase;
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&sh->ring_full[s], ph) && global_timer_ns() - t0 < 1000000ull) {
-        }
-      }
-    }
   }
   __syncwarp();
   return ok;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Copies (warps 18-19, blocks in turn).
+template <class C>
+__device__ __forceinline__ bool copy_role(const ChunkArgs& a, Shared* sh, uint8_t* ring,
+                                          const RingLayout& rl, const Waiter& wait) {
+  const int lane = threadIdx.x & 31, id = (threadIdx.x >> 5) - kWarpCopy;
+  const int kb = C::D * a.c.bits_k / 8, vb = C::D * a.c.bits_v / 8;
+  const int gk = C::D >> a.c.gshift_k, gv = C::D >> a.c.gshift_v;
+  // place of chunk 32 j + lane of the keys' rows of kb / 16 chunks, less 512 j
+  // (32 chunks are whole rows; rows of 8 chunks come in fours, so that j's
+  // lowest bit is bit 2 of the row)
+  const uint32_t dk0 = (lane ^ key_chunk_swizzle(kb / 16, lane >> (__ffs(kb / 16) - 1))) << 4;
+  const uint32_t dk1 = dk0 ^ (kb / 16 == 8 ? 4 << 4 : 0);
+  int slot = 0, turn = 0;
+  uint32_t phase = 0;
+  for (int piece = 0;; ++piece) {
+    if (!wait(&sh->d_full[piece & 1], (piece >> 1) & 1)) return false;
+    const Piece& pd = sh->piece[piece & 1];
+    if (!pd.valid) return true;
+    const int b = pd.b, h = pd.h, first = pd.t0 * C::NT, last = min(pd.lim, pd.t1 * C::NT);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->d_empty[piece & 1]);
+    int page = 0;  // the pages of 32 blocks are looked up at once
+    for (int p = first, i = 0; p < last; p += kBlock, ++i) {
+      if ((i & 31) == 0) {
+        const int q = p + lane * kBlock;
+        page = b;
+        if (a.table != nullptr && q < last) {
+          page = __ldg(a.table + static_cast<size_t>(b) * a.pages_per_seq + (q >> a.page_shift));
+          if (page < 0 || page >= a.c.blocks) {
+            flag_error(a.err, KVQ_DEVERR_BAD_PAGE);
+            page = -1;
+          }
+        }
+      }
+      const int block = __shfl_sync(0xffffffffu, page, i & 31);
+      if (turn == id) {
+        if (!wait(&sh->ring_empty[slot], phase ^ 1)) return false;
+        if (block < 0) {  // (that row's output is unspecified)
+          mbar_arrive(&sh->ring_full[slot]);
+        } else {
+          const int local = a.table != nullptr ? p & ((1 << a.page_shift) - 1) : p;
+          const int cnt = min(kBlock, (last - p + 15) & ~15);  // whole V tiles
+          const size_t row =
+              (static_cast<size_t>(block) * a.c.kv_heads + h) * a.c.block_tokens + local;
+          const uint32_t base = smem_addr(ring + slot * rl.bytes), dst = base + lane * 16;
+          const uint8_t* k = a.c.k_codes + row * kb + lane * 16;
+          const uint8_t* v = a.c.v_codes + row * vb + lane * 16;
+          // (unrolled: one base address each, so that no copy waits until the
+          // one before has taken its address)
+          const int nk = cnt * kb - lane * 16, nv = cnt * vb - lane * 16;
+#pragma unroll
+          for (int j = 0; j < C::D / 16; ++j)
+            if (j * 512 < nk) copy16(base + (j & 1 ? dk1 : dk0) + j * 512, k + j * 512);
+#pragma unroll
+          for (int j = 0; j < C::D / 16; ++j)
+            if (j * 512 < nv) copy16(dst + rl.v + j * 512, v + j * 512);
+          if (lane * 16 < cnt * gk * 4)
+            copy16(dst + rl.kp, reinterpret_cast<const uint8_t*>(a.c.k_params + row * gk) + lane * 16);
+          if (lane * 16 < cnt * gv * 4)
+            copy16(dst + rl.vp, reinterpret_cast<const uint8_t*>(a.c.v_params + row * gv) + lane * 16);
+          // arrives for this lane when its copies are there
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                           smem_addr(&sh->ring_full[slot]))
+                       : "memory");
+        }
+      }
+      turn = turn + 1 == kCopiers ? 0 : turn + 1;
+      if (++slot == rl.blocks) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+  }
 }
 
 // Unpacking (warps 8-15).
@@ -686,7 +702,7 @@ __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint
                                             const uint8_t* ring, const RingLayout& rl,
                                             const Waiter& wait) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
-  const int blk = w / C::HALVES, half = w % C::HALVES;
+  const int blk = w / C::PARTS, part = w % C::PARTS;
   uint64_t* full = KEYS ? sh->k_full : sh->v_full;
   uint64_t* empty = KEYS ? sh->k_empty : sh->v_empty;
   const int gshift = KEYS ? a.c.gshift_k : a.c.gshift_v;
@@ -721,14 +737,14 @@ __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint
         const int live = lim - t * C::NT - blk * kBlock;  // positions of the block that are seen
         if constexpr (KEYS)
           unpack_keys<C, B>(src + rl.k, reinterpret_cast<const uint32_t*>(src + rl.kp), gshift,
-                            lane, half, lane < live, dst, blk * kBlock + lane);
+                            lane, part, lane < live, dst, blk * kBlock + lane);
         else
           unpack_values<C, B>(src + rl.v, reinterpret_cast<const uint32_t*>(src + rl.vp), gshift,
-                              lane, half, live, dst, blk * 4);
+                              lane, part, live, dst, blk * 4);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ring_empty[s]);
       } else {
-        zero_block<C, KEYS>(lane, half, dst, blk);
+        zero_block<C, KEYS>(lane, part, dst, blk);
       }
       fence_proxy_async_shared();
       __syncwarp();
@@ -860,22 +876,27 @@ template <class C, bool ROT>
 __device__ __forceinline__ float load_query(const ChunkArgs& a, size_t off, bool valid,
                                             uint8_t* q, int r) {
   constexpr int D = C::D;
-  auto load8 = [&](int i, float (&x)[8]) {
-    if (!valid) {
+  // A row's 16-byte loads go out together, 32 registers of them at a time
+  // (one by one, the row cost a memory latency each: 24000 cycles).
+  const int es = a.q_dtype == KVQ_F32 ? 4 : 2;
+  const uint4* src =
+      reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + off * es);
+  uint4 raw[8];
+  auto fetch = [&](int part) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = 0.0f;
-    } else if (a.q_dtype == KVQ_F32) {
-      Load8<float>::run(static_cast<const float*>(a.q) + off + 8 * i, x);
-    } else if (a.q_dtype == KVQ_BF16) {
-      Load8<__nv_bfloat16>::run(static_cast<const __nv_bfloat16*>(a.q) + off + 8 * i, x);
-    } else {
-      Load8<__half>::run(static_cast<const __half*>(a.q) + off + 8 * i, x);
-    }
+    for (int i = 0; i < 8; ++i)
+      raw[i] = valid ? __ldg(src + 8 * part + i) : make_uint4(0, 0, 0, 0);
+  };
+  // elements 4j .. 4j + 3 (f32) or 8j .. 8j + 7 of the part as binary32
+  auto half_pair = [&](uint32_t w) {
+    return a.q_dtype == KVQ_BF16
+               ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+               : unpack_half2(w);
   };
   auto scale_of = [](float amax, float& up) {
     int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127 - 14;
     e = max(e, -126);
-    up = pow2i(-e);      // e <= 114
+    up = pow2i(-e);  // e <= 114
     return pow2i(e);
   };
   auto put = [&](int u, const float (&x)[8], float up) {
@@ -893,11 +914,42 @@ __device__ __forceinline__ float load_query(const ChunkArgs& a, size_t off, bool
     store_chunk(dst, hi);
     if constexpr (C::PIECES == 3) store_chunk(dst + C::QTILE, lo);
   };
+  auto widen = [&](int i, float (&x)[8]) {  // 16-bit types: load i of the part
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = half_pair(w[k]);
+      x[2 * k] = f.x;
+      x[2 * k + 1] = f.y;
+    }
+  };
+  auto widen32 = [&](int i, float (&x)[8]) {  // f32: loads 2i, 2i + 1 of the part
+    const uint4 u = raw[2 * i], v = raw[2 * i + 1];
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    x[4] = __uint_as_float(v.x); x[5] = __uint_as_float(v.y);
+    x[6] = __uint_as_float(v.z); x[7] = __uint_as_float(v.w);
+  };
   float amax = 0.0f, up;
   if constexpr (ROT) {  // H q / D, the butterfly h = 1, 2, ..., D/2
     float x[D];
+    if (es == 4) {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) load8(i, *reinterpret_cast<float(*)[8]>(x + 8 * i));
+      for (int part = 0; part < D / 32; ++part) {
+        fetch(part);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          widen32(i, *reinterpret_cast<float(*)[8]>(x + 32 * part + 8 * i));
+      }
+    } else {
+#pragma unroll
+      for (int part = 0; part < D / 64; ++part) {
+        fetch(part);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          widen(i, *reinterpret_cast<float(*)[8]>(x + 64 * part + 8 * i));
+      }
+    }
 #pragma unroll
     for (int h = 1; h < D; h *= 2)
 #pragma unroll
@@ -914,19 +966,40 @@ __device__ __forceinline__ float load_query(const ChunkArgs& a, size_t off, bool
     for (int u = 0; u < D / 8; ++u) put(u, *reinterpret_cast<float(*)[8]>(x + 8 * u), up);
     return down * (1.0f / D);
   } else {
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      float x[8];
-      load8(i, x);
+    const int parts = es == 4 ? D / 32 : D / 64, units = es == 4 ? 4 : 8;  // units of 8 elements
+    float down = 0.0f;
+#pragma unroll 1
+    for (int pass = 0, n = rolled(2); pass < n; ++pass) {  // the maximum, then the values
+#pragma unroll 1
+      for (int part = 0; part < parts; ++part) {
+        fetch(part);
+        if (es == 4) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
-    }
-    const float down = scale_of(amax, up);
-#pragma unroll 4
-    for (int u = 0; u < D / 8; ++u) {
-      float x[8];
-      load8(u, x);
-      put(u, x, up);
+          for (int i = 0; i < 4; ++i) {
+            float x[8];
+            widen32(i, x);
+            if (pass == 0) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
+            } else {
+              put(part * units + i, x, up);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x[8];
+            widen(i, x);
+            if (pass == 0) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
+            } else {
+              put(part * units + i, x, up);
+            }
+          }
+        }
+      }
+      if (pass == 0) down = scale_of(amax, up);
     }
     return down;
   }
@@ -1264,14 +1337,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
       mbar_init(&sh->s_full[i], 1);
       mbar_init(&sh->p_full[i], 4);
       mbar_init(&sh->d_full[i], 1);
-      mbar_init(&sh->d_empty[i], 17);  // softmax 8, keys 4, values 4, MMA 1
+      mbar_init(&sh->d_empty[i], 17 + kCopiers);  // softmax 8, keys 4, values 4, MMA 1, copies
     }
     mbar_init(&sh->q_full, 8);
     mbar_init(&sh->m_full, 4);
     mbar_init(&sh->m_free, 4);
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh->ring_full[i], 1);
-      mbar_init(&sh->ring_empty[i], 2 * C::HALVES);
+      mbar_init(&sh->ring_full[i], 32);
+      mbar_init(&sh->ring_empty[i], 2 * C::PARTS);
     }
     sh->abort = 0;
     fence_barrier_init();
@@ -1316,8 +1389,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kWarpMma) {
       mma_role<C>(sh, smem_addr(smem), __shfl_sync(0xffffffffu, tmem, 0), wait);
-    } else if (warp == kWarpLoad) {
-      load_role<C>(a, sh, ring, rl, pref, wait);
+    } else if (warp == kWarpList) {
+      list_role<C>(a, sh, pref, wait);
+    } else {
+      copy_role<C>(a, sh, ring, rl, wait);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   tc::fence_before_sync();

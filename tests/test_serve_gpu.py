@@ -289,8 +289,10 @@ def test_chunk_bits_and_types(bits, dtype):
                                     (128, 32, 128), (128, 64, 128), (64, 32, 0), (64, 64, 0),
                                     (64, 32, 64)])
 @pytest.mark.parametrize("rot", [False, True])
-def test_chunk_groups(D, G, gv, rot):
-    _chunk_case([150, 40], [30, 40], 4, 2, D, (4, 2), G, gv, 0, rot, "bf16", True)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("bits", [(4, 2), (2, 8), (8, 4)])
+def test_chunk_groups(D, G, gv, rot, dtype, bits):
+    _chunk_case([150, 40], [30, 40], 4, 2, D, bits, G, gv, 0, rot, dtype, True)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
