@@ -504,8 +504,11 @@ __device__ __forceinline__ RingLayout ring_layout(const BlockCache& c, int avail
   l.kp = l.v + kBlock * c.head_dim * c.bits_v / 8;
   l.vp = l.kp + kBlock * (c.head_dim >> c.gshift_k) * 4;
   l.bytes = l.vp + kBlock * (c.head_dim >> c.gshift_v) * 4;
+  // Whole turns of the copiers: each block is always filled by one warp, which
+  // so never waits for a use that is two phases away (a phase bit would not
+  // tell it from the one before).
   l.blocks = 0;
-  while (l.blocks < kRing && (l.blocks + 1) * l.bytes <= avail) ++l.blocks;
+  while (l.blocks < kRing && (l.blocks + kCopiers) * l.bytes <= avail) l.blocks += kCopiers;
   return l;
 }
 
