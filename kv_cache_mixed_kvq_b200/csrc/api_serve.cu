@@ -90,13 +90,14 @@ struct ChunkPlan {
   size_t ml_offset, o_offset, bytes;  // workspace: headers, (m, l), o
 };
 
-// Fewest steps of a CTA's share: below it the set-up of a CTA and the joining
-// of its partial results cost more than the steps.
-constexpr int kMinShare = 2;
+// Steps up to which a unit is not worth dividing: the set-up of a CTA and the
+// joining of its partial results cost more than the steps.
+constexpr int kWholeSteps = 2;
+constexpr int kMinShare = kWholeSteps + kUnitCost;
 
 // Division of work, from the host's bounds alone (the lengths are on the
 // device): one CTA per SM, fewer when there cannot be that much work.  Units
-// of at most kMinShare steps stay whole, which saves the joining launch.
+// of at most kWholeSteps steps stay whole, which saves the joining launch.
 int chunk_plan(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len, int max_seq_len,
                int pieces, ChunkPlan* p) {
   int dev = 0, sms = 0;
@@ -113,10 +114,10 @@ int chunk_plan(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len, i
   const int tile = tile_tokens(pieces, c->head_dim, c->bits_k + c->bits_v);
   const long long tiles = (len + tile - 1) / tile;
   const long long steps = std::max(1ll, rows > 128 && unit > 128 ? tiles : (tiles + 1) / 2);
-  p->whole_units = steps <= kMinShare;
+  p->whole_units = steps <= kWholeSteps;
   p->max_units = static_cast<int>((rows + unit - 1) / unit);
   p->grid = static_cast<int>(std::min<long long>(
-      sms, p->whole_units ? units : (units * steps + kMinShare - 1) / kMinShare));
+      sms, p->whole_units ? units : (units * (steps + kUnitCost) + kMinShare - 1) / kMinShare));
   p->grid = std::max(1, p->grid);
   p->part_rows = static_cast<int>(std::min<long long>(unit, std::max(1ll, rows)));
   const size_t places = static_cast<size_t>(p->grid) * 2;

@@ -73,7 +73,7 @@ static_assert(256 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThre
 constexpr int kRing = 16;         // ring blocks at most
 constexpr int kBlock = 32;        // positions of a ring block
 constexpr int kSmemMax = 232448;  // shared memory a CTA may have (227 KB)
-constexpr int kHeader = 2 * 1024; // barriers, pieces, merge statistics
+constexpr int kHeader = 3 * 1024; // barriers, pieces, merge statistics
 
 template <int D_, int PIECES_, int NT_>
 struct Cfg {
@@ -123,6 +123,7 @@ struct Shared {
   int pad;
   Piece piece[2];
   float2 stat[128];  // narrow merge: slot 1's (m, l)
+  float unscale[2][128];  // of each slot's query rows
 };
 static_assert(sizeof(Shared) <= kHeader, "header");
 
@@ -192,10 +193,11 @@ __device__ __forceinline__ Unit unit_of(const ChunkArgs& a, int n, int len, int 
   return u;
 }
 
-// What a unit counts in the division of work.
+// What a unit counts in the division of work: its steps and what its queries
+// and output take.
 template <class C>
 __device__ __forceinline__ int unit_cost(const ChunkArgs& a, int n, int len, int m) {
-  return a.whole_units ? 1 : unit_of<C>(a, n, len, m).steps;
+  return a.whole_units ? 1 : unit_of<C>(a, n, len, m).steps + kUnitCost;
 }
 
 __device__ __forceinline__ int warp_sum(int v) {
@@ -555,12 +557,17 @@ __device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const 
       within -= __shfl_sync(0xffffffffu, s, 31);
       m += 32;
     }
-    int j = a.whole_units ? 0 : within;
     while (ok && w < w1) {
       const Unit u = unit_of<C>(a, r.n, r.len, m);
-      const int je = a.whole_units
-                         ? u.steps
-                         : static_cast<int>(min(static_cast<long long>(u.steps), j + (w1 - w)));
+      // the share's part [within, upto) of the unit's cost; its first kUnitCost
+      // carry no steps
+      const int cost = a.whole_units ? 1 : u.steps + kUnitCost;
+      const int upto = static_cast<int>(min(static_cast<long long>(cost), within + (w1 - w)));
+      const int j = a.whole_units ? 0 : max(0, within - kUnitCost);
+      const int je = a.whole_units ? u.steps : max(0, upto - kUnitCost);
+      w += upto - within;
+      within = 0;
+      if (je > j) {
       // publish the piece
       ok = wait(&sh->d_empty[piece & 1], ((piece >> 1) & 1) ^ 1);
       if (!ok) break;
@@ -580,9 +587,8 @@ __device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const 
         }
       }
       ++piece;
-      w += a.whole_units ? 1 : je - j;
-      j = 0;
-      if (w < w1 && je == u.steps && ++m == mt) {  // the next row with tokens
+      }
+      if (w < w1 && ++m == mt) {  // the next row with tokens
         m = 0;
         ++b;
         while (true) {
@@ -871,140 +877,89 @@ __device__ __forceinline__ bool mma_role(Shared* sh, uint32_t smem, uint32_t tme
   }
 }
 
-// One row of queries as binary16 (two pieces for PIECES 3), scaled by a power
-// of two that brings its largest magnitude to [2^14, 2^15): bf16 and f16 rows
-// stay exact down to 2^-28 of the largest element.  Returns the factor that
-// undoes it.
+// The queries of a warp's 32 rows as binary16 (two pieces for PIECES 3), each
+// row scaled by a power of two that brings its largest magnitude to
+// [2^14, 2^15): bf16 and f16 rows stay exact down to 2^-28 of the largest
+// element.  unscale[row] undoes it.  A row's elements are taken by D/8
+// consecutive lanes, several rows at once: with a row per lane the loads of a
+// warp touched 32 lines each and took 11000 cycles a unit.  off, valid: of
+// this lane's own row, row0 + lane.
 template <class C, bool ROT>
-__device__ __forceinline__ float load_query(const ChunkArgs& a, size_t off, bool valid,
-                                            uint8_t* q, int r) {
-  constexpr int D = C::D;
-  // A row's 16-byte loads go out together, 32 registers of them at a time
-  // (one by one, the row cost a memory latency each: 24000 cycles).
-  const int es = a.q_dtype == KVQ_F32 ? 4 : 2;
-  const uint4* src =
-      reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + off * es);
-  uint4 raw[8];
-  auto fetch = [&](int part) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      raw[i] = valid ? __ldg(src + 8 * part + i) : make_uint4(0, 0, 0, 0);
-  };
-  // elements 4j .. 4j + 3 (f32) or 8j .. 8j + 7 of the part as binary32
-  auto half_pair = [&](uint32_t w) {
-    return a.q_dtype == KVQ_BF16
-               ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
-               : unpack_half2(w);
-  };
-  auto scale_of = [](float amax, float& up) {
-    int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127 - 14;
-    e = max(e, -126);
-    up = pow2i(-e);  // e <= 114
-    return pow2i(e);
-  };
-  auto put = [&](int u, const float (&x)[8], float up) {
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float y0 = x[2 * c] * up, y1 = x[2 * c + 1] * up;
-      hi[c] = f2_to_h2(y0, y1);
-      if constexpr (C::PIECES == 3) {
-        const float2 h = unpack_half2(hi[c]);
-        lo[c] = f2_to_h2(y0 - h.x, y1 - h.y);
-      }
-    }
-    uint8_t* dst = q + (u / 8) * (128 * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-    store_chunk(dst, hi);
-    if constexpr (C::PIECES == 3) store_chunk(dst + C::QTILE, lo);
-  };
-  auto widen = [&](int i, float (&x)[8]) {  // 16-bit types: load i of the part
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = half_pair(w[k]);
-      x[2 * k] = f.x;
-      x[2 * k + 1] = f.y;
-    }
-  };
-  auto widen32 = [&](int i, float (&x)[8]) {  // f32: loads 2i, 2i + 1 of the part
-    const uint4 u = raw[2 * i], v = raw[2 * i + 1];
-    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
-    x[4] = __uint_as_float(v.x); x[5] = __uint_as_float(v.y);
-    x[6] = __uint_as_float(v.z); x[7] = __uint_as_float(v.w);
-  };
-  float amax = 0.0f, up;
-  if constexpr (ROT) {  // H q / D, the butterfly h = 1, 2, ..., D/2
-    float x[D];
-    if (es == 4) {
-#pragma unroll
-      for (int part = 0; part < D / 32; ++part) {
-        fetch(part);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          widen32(i, *reinterpret_cast<float(*)[8]>(x + 32 * part + 8 * i));
-      }
-    } else {
-#pragma unroll
-      for (int part = 0; part < D / 64; ++part) {
-        fetch(part);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          widen(i, *reinterpret_cast<float(*)[8]>(x + 64 * part + 8 * i));
-      }
-    }
-#pragma unroll
-    for (int h = 1; h < D; h *= 2)
-#pragma unroll
-      for (int i = 0; i < D; ++i)
-        if ((i & h) == 0) {
-          const float y = x[i], z = x[i + h];
-          x[i] = y + z;
-          x[i + h] = y - z;
-        }
-#pragma unroll
-    for (int i = 0; i < D; ++i) amax = fmaxf(amax, fabsf(x[i]));
-    const float down = scale_of(amax, up);
-#pragma unroll
-    for (int u = 0; u < D / 8; ++u) put(u, *reinterpret_cast<float(*)[8]>(x + 8 * u), up);
-    return down * (1.0f / D);
-  } else {
-    const int parts = es == 4 ? D / 32 : D / 64, units = es == 4 ? 4 : 8;  // units of 8 elements
-    float down = 0.0f;
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, size_t off, bool valid,
+                                             uint8_t* q, float* unscale, int row0) {
+  constexpr int D = C::D, LANES = D / 8, ROWS = 32 / LANES;  // of a row; rows at once
+  const int lane = threadIdx.x & 31, u = lane % LANES;
+  const bool f32 = a.q_dtype == KVQ_F32;
+  const int turns = f32 ? 4 : 8;  // eight loads at a time
+  const uint32_t kinds = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
-    for (int pass = 0, n = rolled(2); pass < n; ++pass) {  // the maximum, then the values
+  for (int t0 = 0; t0 < LANES; t0 += turns) {
+    uint4 raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = (t0 + (f32 ? i / 2 : i)) * ROWS + lane / LANES;
+      const size_t at = __shfl_sync(0xffffffffu, off, row) + 8 * u;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if ((kinds >> row) & 1)
+        raw[i] = f32 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at) +
+                             (i & 1))
+                     : __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+    }
 #pragma unroll 1
-      for (int part = 0; part < parts; ++part) {
-        fetch(part);
-        if (es == 4) {
+    for (int t = t0; t < t0 + turns; ++t) {
+      float x[8];
+      const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
+                             raw[1].x, raw[1].y, raw[1].z, raw[1].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x[8];
-            widen32(i, x);
-            if (pass == 0) {
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t h = k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu;
+        x[k] = f32                      ? __uint_as_float(w[k])
+               : a.q_dtype == KVQ_BF16 ? __uint_as_float(h << 16)
+                                       : __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+      }
 #pragma unroll
-              for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
-            } else {
-              put(part * units + i, x, up);
+      for (int i = 0; i < 7; ++i) raw[i] = f32 && i < 6 ? raw[i + 2] : raw[i + 1];
+      if constexpr (ROT) {  // H q / D, the butterfly h = 1, 2, ..., D/2
+#pragma unroll
+        for (int h = 1; h < 8; h *= 2)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((i & h) == 0) {
+              const float y = x[i], z = x[i + h];
+              x[i] = y + z;
+              x[i + h] = y - z;
             }
-          }
-        } else {
+#pragma unroll
+        for (int m = 1; m < LANES; m *= 2)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float x[8];
-            widen(i, x);
-            if (pass == 0) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
-            } else {
-              put(part * units + i, x, up);
-            }
+            const float y = __shfl_xor_sync(0xffffffffu, x[i], m);
+            x[i] = u & m ? y - x[i] : y + x[i];
           }
+      }
+      float amax = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
+#pragma unroll
+      for (int m = 1; m < LANES; m *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+      const int e = max(static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127 - 14, -126);
+      const float up = pow2i(-e);  // e <= 114
+      const int r = row0 + t * ROWS + lane / LANES;
+      if (u == 0) unscale[r] = pow2i(e) * (ROT ? 1.0f / D : 1.0f);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float y0 = x[2 * c] * up, y1 = x[2 * c + 1] * up;
+        hi[c] = f2_to_h2(y0, y1);
+        if constexpr (C::PIECES == 3) {
+          const float2 h = unpack_half2(hi[c]);
+          lo[c] = f2_to_h2(y0 - h.x, y1 - h.y);
         }
       }
-      if (pass == 0) down = scale_of(amax, up);
+      uint8_t* dst = q + (u / 8) * (128 * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+      store_chunk(dst, hi);
+      if constexpr (C::PIECES == 3) store_chunk(dst + C::QTILE, lo);
     }
-    return down;
   }
 }
 
@@ -1102,18 +1057,16 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
     float unscale = 1.0f;
     if (wide || slot == 0) {
       if (works)
-        unscale = load_query<C, ROT>(
+        load_queries<C, ROT>(
             a, static_cast<size_t>(token) * a.q_stride + static_cast<size_t>(head) * D, valid,
-            smem + (wide ? slot * C::QTILE : 0), r);
+            smem + (wide ? slot * C::QTILE : 0), sh->unscale[wide ? slot : 0], r & ~31);
       fence_proxy_async_shared();
     }
-    if (!wide && slot == 0) sh->stat[r].x = unscale;  // slot 1 has the same rows
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->q_full);
-    if (!wide && slot == 1) {
-      if (!wait(&sh->q_full, piece & 1)) return false;
-      unscale = sh->stat[r].x;
-    }
+    // (a narrow unit's slot 1 has the rows of slot 0)
+    if (!wide && slot == 1 && !wait(&sh->q_full, piece & 1)) return false;
+    if (works) unscale = sh->unscale[wide ? slot : 0][r];
     // scores in units of log2: S * c
     const float c = fmaxf(a.sm_scale_log2 * unscale, 1.2e-38f);
     float m = -INFINITY, l = 0.0f;
@@ -1263,17 +1216,22 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       }
     }
     if ((wide || slot == 0) && works) {
-      float* po = nullptr;
       if (whole) {
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         f0 *= inv;
         f1 *= inv;
-      } else {
-        const size_t prow = static_cast<size_t>(blockIdx.x * 2 + part) * a.part_rows + ur;
-        po = a.ws_o + prow * D;
-        if (valid) a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, l);
       }
-      const size_t orow = (static_cast<size_t>(token) * a.q_heads + head) * D;
+      // the row's place in the output, or among the partial results
+      const size_t prow = static_cast<size_t>(blockIdx.x * 2 + part) * a.part_rows + ur;
+      if (!whole && valid) a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, l);
+      const int type = whole ? a.out_dtype : static_cast<int>(KVQ_F32);
+      const size_t row = whole ? (static_cast<size_t>(token) * a.q_heads + head) * D : prow * D;
+      uint8_t* dst = (whole ? static_cast<uint8_t*>(a.out) : reinterpret_cast<uint8_t*>(a.ws_o)) +
+                     row * (type == KVQ_F32 ? 4 : 2);
+      // A wide unit's rows go through the slot's query tile, 32 columns at a
+      // time, so that a store covers whole sectors of few rows.
+      uint8_t* stage = smem + slot * C::QTILE + (warp & 3) * (C::QTILE / 4);
+      const uint32_t rows_valid = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
       for (int i = 0, in = rolled(D / 32); i < in; ++i) {
         uint32_t o[32];
@@ -1284,11 +1242,15 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0;
         }
+        const int cs = type == KVQ_F32 ? 3 : 2;  // log2 of the row's 16-byte chunks
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * k + e]) * f0;
+          for (int e = 0; e < 8; ++e) {
+            x[e] = __uint_as_float(o[8 * k + e]) * f0;
+            if (whole && !(l > 0.0f)) x[e] = 0.0f;  // (no position is seen)
+          }
           if (other) {
             const float4 y = merge[(8 * i + 2 * k) ^ (r & 7)], z = merge[(8 * i + 2 * k + 1) ^ (r & 7)];
             x[0] = fmaf(y.x, f1, x[0]); x[1] = fmaf(y.y, f1, x[1]);
@@ -1296,19 +1258,31 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
             x[4] = fmaf(z.x, f1, x[4]); x[5] = fmaf(z.y, f1, x[5]);
             x[6] = fmaf(z.z, f1, x[6]); x[7] = fmaf(z.w, f1, x[7]);
           }
-          if (valid) {
-            if (whole) {
-              if (!(l > 0.0f)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-              }
-              store_out8(a.out, a.out_dtype, orow + 32 * i + 8 * k, x);
+          if (wide) {
+            if (type == KVQ_F32) {
+              float4* d = reinterpret_cast<float4*>(stage + lane * 128);
+              d[(2 * k) ^ (lane & 7)] = make_float4(x[0], x[1], x[2], x[3]);
+              d[(2 * k + 1) ^ (lane & 7)] = make_float4(x[4], x[5], x[6], x[7]);
             } else {
-              float4* d = reinterpret_cast<float4*>(po + 32 * i + 8 * k);
-              d[0] = make_float4(x[0], x[1], x[2], x[3]);
-              d[1] = make_float4(x[4], x[5], x[6], x[7]);
+              store_out8(stage, type, (lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) / 2, x);
             }
+          } else if (valid) {
+            store_out8(dst, type, 32 * i + 8 * k, x);
           }
+        }
+        if (wide) {
+          __syncwarp();
+#pragma unroll 1
+          for (int y = lane; y < 32 << cs; y += 32) {
+            const int rr = y >> cs, ch = y & ((1 << cs) - 1);
+            const int sw = cs == 3 ? ch ^ (rr & 7) : ch ^ ((rr >> 1) & 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + (((rr << cs) + sw) << 4));
+            uint8_t* to = reinterpret_cast<uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
+            if ((rows_valid >> rr) & 1)
+              *reinterpret_cast<uint4*>(to + (((i << cs) + ch) << 4)) = v;
+          }
+          __syncwarp();
         }
       }
     }

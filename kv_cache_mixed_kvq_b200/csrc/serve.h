@@ -62,6 +62,9 @@ constexpr int unit_rows(int pieces) { return pieces == 3 ? 128 : 256; }
 constexpr int tile_tokens(int pieces, int head_dim, int bits_kv) {
   return pieces == 1 && !(head_dim == 128 && bits_kv == 16) ? 128 : 64;
 }
+// Steps that a unit's queries and output are worth in the division of work (8 to
+// 10 thousand cycles on B200, a step about 5).
+constexpr int kUnitCost = 2;
 // Batch rows one call takes (their prefix sums lie in the tiles' memory).
 constexpr int kChunkRows = 16384;
 
