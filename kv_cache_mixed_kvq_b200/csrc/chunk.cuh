@@ -24,15 +24,15 @@
 //      hi lo + lo hi, 2^-22 in all.
 // Softmax statistics, sums and outputs are binary32.
 //
-// Roles (20 warps, one CTA per SM):
-//   warps 0-7   softmax: two slots of four warps; one thread a row of its slot
-//   warps 8-11  keys: packed codes from the ring to a K tile (binary16,
+// Roles (28 warps, one CTA per SM):
+//   warps 0-15  softmax: two slots of eight warps; two threads a row of a slot
+//   warps 16-19 keys: packed codes from the ring to a K tile (binary16,
 //               128-byte swizzle)
-//   warps 12-15 values: the same to a V tile (rows are elements: K-major along
+//   warps 20-23 values: the same to a V tile (rows are elements: K-major along
 //               the positions, which is the order of the packed V tiles)
-//   warp 16     issues the MMAs
-//   warp 17     walks the work list and publishes each piece of work
-//   warps 18-19 copy packed codes and parameters, 32 positions at a time, into
+//   warp 24     issues the MMAs
+//   warp 25     walks the work list and publishes each piece of work
+//   warps 26-27 copy packed codes and parameters, 32 positions at a time, into
 //               the ring (cp.async: four bulk copies a block, each set up in
 //               uniform registers, took 900 cycles of the one warp)
 // In a wide unit (more than 128 rows) the slots are its two halves and share
@@ -61,19 +61,19 @@
 namespace kvq {
 namespace chunk {
 
-constexpr int kThreads = 20 * 32;
-constexpr int kWarpsK = 8, kWarpsV = 12, kWarpMma = 16, kWarpList = 17, kWarpCopy = 18;
+constexpr int kThreads = 28 * 32;
+constexpr int kWarpsK = 16, kWarpsV = 20, kWarpMma = 24, kWarpList = 25, kWarpCopy = 26;
 constexpr int kCopiers = 2;       // warps that copy, block by block in turn
-// Registers a thread at launch, and of each warpgroup after the split: the
-// softmax groups take what the others give, 256 x 128 + 256 x 80 + 128 x 64
-// = 640 x 96.  (Five warps share an SM quarter's 16384 registers, hence 96.)
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsUnpack = 80, kRegsIssue = 64;
-static_assert(256 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThreads * kRegsLaunch,
+// Registers a thread at launch, and of each warpgroup after the split: 512 x 80
+// + 256 x 64 + 128 x 56 <= 896 x 72.  (Seven warps share an SM quarter's 16384
+// registers, hence 72.)
+constexpr int kRegsLaunch = 72, kRegsSoftmax = 80, kRegsUnpack = 64, kRegsIssue = 56;
+static_assert(512 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThreads * kRegsLaunch,
               "more registers than the launch has would never be granted");
 constexpr int kRing = 16;         // ring blocks at most
 constexpr int kBlock = 32;        // positions of a ring block
 constexpr int kSmemMax = 232448;  // shared memory a CTA may have (227 KB)
-constexpr int kHeader = 3 * 1024; // barriers, pieces, merge statistics
+constexpr int kHeader = 7 * 1024; // barriers, pieces, merge statistics
 
 template <int D_, int PIECES_, int NT_>
 struct Cfg {
@@ -115,6 +115,7 @@ struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2];
   uint64_t q_full, m_full, m_free;
+  uint64_t x_full[2][4];  // [slot][quarter of the rows]: the two halves' maxima
   uint64_t d_full[2], d_empty[2];
   uint64_t ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
@@ -124,6 +125,7 @@ struct Shared {
   Piece piece[2];
   float2 stat[128];  // narrow merge: slot 1's (m, l)
   float unscale[2][128];  // of each slot's query rows
+  float top[2][2][2][128];  // [slot][turn][half of the columns]: maxima or sums
 };
 static_assert(sizeof(Shared) <= kHeader, "header");
 
@@ -514,7 +516,7 @@ __device__ __forceinline__ RingLayout ring_layout(const BlockCache& c, int avail
   return l;
 }
 
-// Work list (warp 17).
+// Work list (warp 25).
 template <class C>
 __device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const int* pref,
                                           const Waiter& wait) {
@@ -630,7 +632,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Copies (warps 18-19, blocks in turn).
+// Copies (warps 26-27, blocks in turn).
 template <class C>
 __device__ __forceinline__ bool copy_role(const ChunkArgs& a, Shared* sh, uint8_t* ring,
                                           const RingLayout& rl, const Waiter& wait) {
@@ -705,7 +707,7 @@ __device__ __forceinline__ bool copy_role(const ChunkArgs& a, Shared* sh, uint8_
   }
 }
 
-// Unpacking (warps 8-15).
+// Unpacking (warps 16-23).
 template <class C, bool KEYS, int B>
 __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint8_t* tiles,
                                             const uint8_t* ring, const RingLayout& rl,
@@ -767,7 +769,7 @@ __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint
   }
 }
 
-// MMA issue (warp 16; operands are uniform over the warp, one lane issues).
+// MMA issue (warp 24; operands are uniform over the warp, one lane issues).
 template <class C>
 __device__ __forceinline__ void issue_scores(uint32_t s_tmem, uint32_t q, uint32_t k) {
   constexpr uint32_t idesc = tc::idesc_f16_kk(128, C::NT);
@@ -797,17 +799,15 @@ __device__ __forceinline__ void issue_output(uint32_t o_tmem, uint32_t p_tmem, u
   const uint64_t v0 = tc::smem_desc_k128(v);
 #pragma unroll 1
   for (int x = C::PIECES - 1; x >= 0; --x) {
-    uint32_t pa = p_tmem + (x == 2 ? C::NT / 2 : 0);
-    uint64_t va = v0 + (x == 1 ? C::KPIECE >> 4 : 0);
-#pragma unroll 1
-    for (int i = 0, in = rolled(C::NT / 64); i < in; ++i) {
+    // the weights of each half of the positions start at that half's columns
+    const uint32_t pa = p_tmem + (x == 2 ? C::NT / 4 : 0);
+    const uint64_t va = v0 + (x == 1 ? C::KPIECE >> 4 : 0);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        tc::mma_f16_ts(o_tmem, pa + 8 * y, va + 2 * y, idesc, accumulate);
-        accumulate = true;
-      }
-      pa += 32;
-      va += (C::D * 128) >> 4;
+    for (int i = 0; i < C::NT / 16; ++i) {
+      constexpr int HALF = C::NT / 32;  // steps of 16 positions in a half
+      tc::mma_f16_ts(o_tmem, pa + (i / HALF) * (C::NT / 2) + (i % HALF) * 8,
+                     va + (i / 4) * ((C::D * 128) >> 4) + (i % 4) * 2, idesc, accumulate);
+      accumulate = true;
     }
   }
 }
@@ -877,7 +877,7 @@ __device__ __forceinline__ bool mma_role(Shared* sh, uint32_t smem, uint32_t tme
   }
 }
 
-// The queries of a warp's 32 rows as binary16 (two pieces for PIECES 3), each
+// Half of the queries of a warp's 32 rows as binary16 (two pieces for PIECES 3), each
 // row scaled by a power of two that brings its largest magnitude to
 // [2^14, 2^15): bf16 and f16 rows stay exact down to 2^-28 of the largest
 // element.  unscale[row] undoes it.  A row's elements are taken by D/8
@@ -886,18 +886,18 @@ __device__ __forceinline__ bool mma_role(Shared* sh, uint32_t smem, uint32_t tme
 // this lane's own row, row0 + lane.
 template <class C, bool ROT>
 __device__ __forceinline__ void load_queries(const ChunkArgs& a, size_t off, bool valid,
-                                             uint8_t* q, float* unscale, int row0) {
+                                             uint8_t* q, float* unscale, int row0, int half) {
   constexpr int D = C::D, LANES = D / 8, ROWS = 32 / LANES;  // of a row; rows at once
   const int lane = threadIdx.x & 31, u = lane % LANES;
   const bool f32 = a.q_dtype == KVQ_F32;
-  const int turns = f32 ? 4 : 8;  // eight loads at a time
+  const int turns = f32 || LANES < 16 ? 4 : 8;  // eight loads at a time, at most
   const uint32_t kinds = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
-  for (int t0 = 0; t0 < LANES; t0 += turns) {
+  for (int t0 = half * LANES / 2; t0 < (half + 1) * LANES / 2; t0 += turns) {
     uint4 raw[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int row = (t0 + (f32 ? i / 2 : i)) * ROWS + lane / LANES;
+      const int row = ((t0 + (f32 ? i / 2 : i)) * ROWS + lane / LANES) & 31;
       const size_t at = __shfl_sync(0xffffffffu, off, row) + 8 * u;
       raw[i] = make_uint4(0, 0, 0, 0);
       if ((kinds >> row) & 1)
@@ -1018,17 +1018,32 @@ __device__ __forceinline__ float sum_of(uint64_t s) {
   return x + y;
 }
 
-// Softmax of one slot (warps 0-3: slot 0, 4-7: slot 1).
+// Softmax (warps 0-7: slot 0, 8-15: slot 1).  A thread has one row and half of a
+// tile's columns, as of the output's elements: with whole rows a slot's tile
+// took twice as long, and between two products of a slot lies its softmax.
+// The two warps of 32 rows agree on the maxima through shared memory.
 template <class C, bool ROT>
 __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uint8_t* smem,
                                              uint32_t tmem, const Waiter& wait) {
-  constexpr int D = C::D, NT = C::NT;
+  constexpr int D = C::D, NH = C::NT / 2, DH = D / 2;  // this thread's columns
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int slot = warp >> 2, r = threadIdx.x & 127;  // row of the slot
-  const uint32_t quad = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const uint32_t s_tmem = tmem + quad + slot * C::S_COL;
-  const uint32_t o_tmem = tmem + quad + C::O_BASE + slot * C::O_COL;
-  uint32_t s_phase = 0, merges = 0;
+  const int slot = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+  const int r = quarter * 32 + lane;  // row of the slot
+  const uint32_t quad = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t s_tmem = tmem + quad + slot * C::S_COL + half * NH;
+  const uint32_t o_tmem = tmem + quad + C::O_BASE + slot * C::O_COL + half * DH;
+  uint32_t s_phase = 0, merges = 0, turn = 0;
+  // Exchange of a value with the row's other thread.  Two turns' places: a
+  // warp that is a turn ahead does not overwrite what the other still reads.
+  auto other_half = [&](float mine, float& theirs) {
+    sh->top[slot][turn & 1][half][r] = mine;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->x_full[slot][quarter]);
+    if (!wait(&sh->x_full[slot][quarter], turn & 1)) return false;
+    theirs = sh->top[slot][turn & 1][half ^ 1][r];
+    ++turn;
+    return true;
+  };
   for (int piece = 0;; ++piece) {
     if (!wait(&sh->d_full[piece & 1], (piece >> 1) & 1)) return false;
     const Piece& pd = sh->piece[piece & 1];
@@ -1052,21 +1067,18 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       t = 2 * j0 + slot; tend = t1; stride = 2;
     }
     const bool any_tile = t < tend;
-    const bool works = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps pace
-    // ---- queries
-    float unscale = 1.0f;
-    if (wide || slot == 0) {
-      if (works)
-        load_queries<C, ROT>(
-            a, static_cast<size_t>(token) * a.q_stride + static_cast<size_t>(head) * D, valid,
-            smem + (wide ? slot * C::QTILE : 0), sh->unscale[wide ? slot : 0], r & ~31);
+    const bool works = __any_sync(0xffffffffu, valid);  // warps without rows only keep pace
+    // ---- queries (a narrow unit's slot 1 has the rows of slot 0)
+    if ((wide || slot == 0) && works) {
+      load_queries<C, ROT>(
+          a, static_cast<size_t>(token) * a.q_stride + static_cast<size_t>(head) * D, valid,
+          smem + (wide ? slot * C::QTILE : 0), sh->unscale[wide ? slot : 0], quarter * 32, half);
       fence_proxy_async_shared();
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->q_full);
-    // (a narrow unit's slot 1 has the rows of slot 0)
-    if (!wide && slot == 1 && !wait(&sh->q_full, piece & 1)) return false;
-    if (works) unscale = sh->unscale[wide ? slot : 0][r];
+    if (!wait(&sh->q_full, piece & 1)) return false;
+    const float unscale = works ? sh->unscale[wide ? slot : 0][r] : 1.0f;
     // scores in units of log2: S * c
     const float c = fmaxf(a.sm_scale_log2 * unscale, 1.2e-38f);
     float m = -INFINITY, l = 0.0f;
@@ -1079,10 +1091,10 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
         // (One pass with the weights held in registers until the maximum is
         // known was slower: its loop, unrolled over the registers, does not
         // stay in the instruction cache beside the other roles'.)
-        const int seen = limit - t * NT;
-        if (__any_sync(0xffffffffu, seen < NT)) {  // masked: -inf in place
+        const int seen = limit - t * C::NT - half * NH;
+        if (__any_sync(0xffffffffu, seen < NH)) {  // masked: -inf in place
 #pragma unroll 1
-          for (int i = 0, in = rolled(NT / 16); i < in; ++i) {
+          for (int i = 0, in = rolled(NH / 16); i < in; ++i) {
             uint32_t s[16];
             tc::ld_32x32b<16>(s_tmem + 16 * i, s);
             tc::wait_ld(s);
@@ -1093,33 +1105,39 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
           }
           tc::wait_st();
         }
-        float mx = m;
+        uint32_t s[2][16];  // 16 scores at a time, the next ones on their way
+        float mx;
         {
-          uint32_t s[2][16];  // 16 scores at a time, the next ones on their way
+          float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};  // (a chain each)
           tc::ld_32x32b<16>(s_tmem, s[0]);
 #pragma unroll 1
-          for (int i = 0, in = rolled(NT / 32); i < in; ++i) {
+          for (int i = 0, in = rolled(NH / 32); i < in; ++i) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               tc::wait_ld(s[x]);
-              // (the last read wraps round)
-              tc::ld_32x32b<16>(s_tmem + ((32 * i + 16 * x + 16) & (NT - 1)), s[x ^ 1]);
+              // (the last read wraps round to the first scores, for the weights)
+              tc::ld_32x32b<16>(s_tmem + ((32 * i + 16 * x + 16) & (NH - 1)), s[x ^ 1]);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(s[x][k]));
+              for (int k = 0; k < 8; ++k)
+                top[k & 3] = fmaxf(top[k & 3], fmaxf(__uint_as_float(s[x][2 * k]),
+                                                     __uint_as_float(s[x][2 * k + 1])));
             }
           }
-          tc::wait_ld(s[0]);
+          float theirs;
+          mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          if (!other_half(mx, theirs)) return false;
+          mx = fmaxf(mx, theirs);
         }
         if (first) {
           m = mx;
         } else if (__any_sync(0xffffffffu, (mx - m) * c > C::kThreshold)) {
-          // (false while nothing is seen) every row moves to its maximum, and
-          // its sums follow
+          // (false while nothing is seen; the same in both warps) every row
+          // moves to its maximum, and its sums follow
           const float f = mx == -INFINITY ? 1.0f : exp2_approx((m - mx) * c);
           l *= f;
           m = mx;
 #pragma unroll 1
-          for (int i = 0, in = rolled(D / 16); i < in; ++i) {
+          for (int i = 0, in = rolled(DH / 16); i < in; ++i) {
             uint32_t o[16];
             tc::ld_32x32b<16>(o_tmem + 16 * i, o);
             tc::wait_ld(o);
@@ -1130,23 +1148,22 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
         }
         const float shift = C::kOffset - (m == -INFINITY ? 0.0f : m * c);
         const uint64_t c2 = pair(c, c), shift2 = pair(shift, shift);
-        uint64_t sum2 = 0;
+        uint64_t sum2[2] = {0, 0};
         if constexpr (C::PIECES < 3) {
-          uint32_t s[2][16];  // (a chunk's weights take columns that were read)
-          tc::ld_32x32b<16>(s_tmem, s[0]);
+          // (a chunk's weights take columns that were read)
 #pragma unroll 1
-          for (int i = 0, in = rolled(NT / 32); i < in; ++i) {
+          for (int i = 0, in = rolled(NH / 32); i < in; ++i) {
             uint32_t p[16];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               tc::wait_ld(s[x]);
-              if (x == 0 || i + 1 < NT / 32)
+              if (x == 0 || i + 1 < in)
                 tc::ld_32x32b<16>(s_tmem + 32 * i + 16 * x + 16, s[x ^ 1]);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 uint32_t none;
-                weights<C::PIECES>(s[x][2 * k], s[x][2 * k + 1], c2, shift2, sum2, p[8 * x + k],
-                                   none);
+                weights<C::PIECES>(s[x][2 * k], s[x][2 * k + 1], c2, shift2, sum2[k & 1],
+                                   p[8 * x + k], none);
               }
             }
             tc::st_32x32b_x16(s_tmem + 16 * i, p);
@@ -1154,24 +1171,19 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
         } else {
           // two binary16 pieces take a score's column each: all scores are
           // read before the first are written
-          uint32_t s[NT];
+          static_assert(C::PIECES < 3 || NH == 32, "the scores of half a tile in two loads");
+          tc::ld_32x32b<16>(s_tmem + 16, s[1]);
+          tc::wait_ld(s[0]);
+          tc::wait_ld(s[1]);
+          uint32_t p[16], q[16];
 #pragma unroll
-          for (int i = 0; i < NT / 32; ++i)
-            tc::ld_32x32b<32>(s_tmem + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
-#pragma unroll
-          for (int i = 0; i < NT / 32; ++i)
-            tc::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
-#pragma unroll
-          for (int i = 0; i < NT / 32; ++i) {
-            uint32_t p[16], q[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              weights<3>(s[32 * i + 2 * k], s[32 * i + 2 * k + 1], c2, shift2, sum2, p[k], q[k]);
-            tc::st_32x32b_x16(s_tmem + 16 * i, p);
-            tc::st_32x32b_x16(s_tmem + NT / 2 + 16 * i, q);
-          }
+          for (int k = 0; k < 16; ++k)
+            weights<3>(s[k / 8][2 * (k % 8)], s[k / 8][2 * (k % 8) + 1], c2, shift2, sum2[k & 1],
+                       p[k], q[k]);
+          tc::st_32x32b_x16(s_tmem, p);
+          tc::st_32x32b_x16(s_tmem + NH / 2, q);
         }
-        l += sum_of(sum2);
+        l += sum_of(sum2[0]) + sum_of(sum2[1]);
         tc::wait_st();
       }
       tc::fence_before_sync();
@@ -1184,25 +1196,31 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       s_phase ^= 1;
       tc::fence_after_sync();
     }
+    if (works) {  // the row's whole sum
+      float theirs;
+      if (!other_half(l, theirs)) return false;
+      l = half == 0 ? l + theirs : theirs + l;
+    }
     float f0 = 1.0f, f1 = 0.0f;
-    float4* merge = reinterpret_cast<float4*>(smem) + r * (D / 4);  // slot 1's row, swizzled
-    const bool other = !wide && 2 * j0 + 1 < t1;                    // slot 1 has an output
+    // slot 1's row (this half of it), swizzled
+    float4* merge = reinterpret_cast<float4*>(smem) + r * (D / 4) + half * (DH / 4);
+    const bool other = !wide && 2 * j0 + 1 < t1;  // slot 1 has an output
     if (!wide) {
       if (slot == 1) {
         if (other && works) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tc::ld_32x32b<32>(o_tmem + 32 * i, o);
+#pragma unroll 1
+          for (int i = 0, in = rolled(DH / 16); i < in; ++i) {
+            uint32_t o[16];
+            tc::ld_32x32b<16>(o_tmem + 16 * i, o);
             tc::wait_ld(o);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              merge[(8 * i + k) ^ (r & 7)] =
+            for (int k = 0; k < 4; ++k)
+              merge[(4 * i + k) ^ (r & 7)] =
                   make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                               __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
           }
         }
-        sh->stat[r] = make_float2(m, l);
+        if (half == 0) sh->stat[r] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->m_full);
       } else {
@@ -1217,66 +1235,68 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
     }
     if ((wide || slot == 0) && works) {
       if (whole) {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // (0: no position is seen)
         f0 *= inv;
         f1 *= inv;
       }
       // the row's place in the output, or among the partial results
       const size_t prow = static_cast<size_t>(blockIdx.x * 2 + part) * a.part_rows + ur;
-      if (!whole && valid) a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, l);
+      if (!whole && valid && half == 0)
+        a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, l);
       const int type = whole ? a.out_dtype : static_cast<int>(KVQ_F32);
       const size_t row = whole ? (static_cast<size_t>(token) * a.q_heads + head) * D : prow * D;
+      const int es = type == KVQ_F32 ? 4 : 2;
       uint8_t* dst = (whole ? static_cast<uint8_t*>(a.out) : reinterpret_cast<uint8_t*>(a.ws_o)) +
-                     row * (type == KVQ_F32 ? 4 : 2);
-      // A wide unit's rows go through the slot's query tile, 32 columns at a
-      // time, so that a store covers whole sectors of few rows.
-      uint8_t* stage = smem + slot * C::QTILE + (warp & 3) * (C::QTILE / 4);
+                     (row + half * DH) * es;
+      // A wide unit's rows go through the slot's query tile, 16 columns at a
+      // time, so that a store covers whole sectors of many rows.
+      uint8_t* stage = smem + slot * C::QTILE + (quarter * 2 + half) * (C::QTILE / 8);
       const uint32_t rows_valid = __ballot_sync(0xffffffffu, valid);
+      const bool nothing = whole && !(l > 0.0f);
 #pragma unroll 1
-      for (int i = 0, in = rolled(D / 32); i < in; ++i) {
-        uint32_t o[32];
+      for (int i = 0, in = rolled(DH / 16); i < in; ++i) {
+        uint32_t o[16];
         if (any_tile) {
-          tc::ld_32x32b<32>(o_tmem + 32 * i, o);
+          tc::ld_32x32b<16>(o_tmem + 16 * i, o);
           tc::wait_ld(o);
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
+          for (int k = 0; k < 16; ++k) o[k] = 0;
         }
-        const int cs = type == KVQ_F32 ? 3 : 2;  // log2 of the row's 16-byte chunks
+        const int cs = es == 4 ? 2 : 1;  // log2 of 16-byte chunks in 16 columns
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] = __uint_as_float(o[8 * k + e]) * f0;
-            if (whole && !(l > 0.0f)) x[e] = 0.0f;  // (no position is seen)
-          }
+          for (int e = 0; e < 8; ++e) x[e] = nothing ? 0.0f : __uint_as_float(o[8 * k + e]) * f0;
           if (other) {
-            const float4 y = merge[(8 * i + 2 * k) ^ (r & 7)], z = merge[(8 * i + 2 * k + 1) ^ (r & 7)];
+            const float4 y = merge[(4 * i + 2 * k) ^ (r & 7)];
+            const float4 z = merge[(4 * i + 2 * k + 1) ^ (r & 7)];
             x[0] = fmaf(y.x, f1, x[0]); x[1] = fmaf(y.y, f1, x[1]);
             x[2] = fmaf(y.z, f1, x[2]); x[3] = fmaf(y.w, f1, x[3]);
             x[4] = fmaf(z.x, f1, x[4]); x[5] = fmaf(z.y, f1, x[5]);
             x[6] = fmaf(z.z, f1, x[6]); x[7] = fmaf(z.w, f1, x[7]);
           }
-          if (wide) {
-            if (type == KVQ_F32) {
-              float4* d = reinterpret_cast<float4*>(stage + lane * 128);
-              d[(2 * k) ^ (lane & 7)] = make_float4(x[0], x[1], x[2], x[3]);
-              d[(2 * k + 1) ^ (lane & 7)] = make_float4(x[4], x[5], x[6], x[7]);
+          if (wide) {  // rows of 64 bytes; chunk c of row r at c ^ (r / 2 mod 4)
+            const int sw = (lane >> 1) & 3;
+            if (es == 4) {
+              float4* d = reinterpret_cast<float4*>(stage + lane * 64);
+              d[(2 * k) ^ sw] = make_float4(x[0], x[1], x[2], x[3]);
+              d[(2 * k + 1) ^ sw] = make_float4(x[4], x[5], x[6], x[7]);
             } else {
-              store_out8(stage, type, (lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) / 2, x);
+              store_out8(stage, type, (lane * 64 + ((k ^ sw) << 4)) / 2, x);
             }
           } else if (valid) {
-            store_out8(dst, type, 32 * i + 8 * k, x);
+            store_out8(dst, type, 16 * i + 8 * k, x);
           }
         }
         if (wide) {
           __syncwarp();
-#pragma unroll 1
+#pragma unroll 2
           for (int y = lane; y < 32 << cs; y += 32) {
             const int rr = y >> cs, ch = y & ((1 << cs) - 1);
-            const int sw = cs == 3 ? ch ^ (rr & 7) : ch ^ ((rr >> 1) & 3);
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + (((rr << cs) + sw) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 +
+                                                            ((ch ^ ((rr >> 1) & 3)) << 4));
             uint8_t* to = reinterpret_cast<uint8_t*>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
             if ((rows_valid >> rr) & 1)
@@ -1287,12 +1307,11 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       }
     }
     tc::fence_before_sync();
-    if (!wide) {  // the merge buffer is the query tiles' memory
-      __syncwarp();
-      if (slot == 0 && lane == 0) mbar_arrive(&sh->m_free);
-      if (!wait(&sh->m_free, merges & 1)) return false;
-      ++merges;
-    }
+    // the rows on their way to the output lie in the query tiles' memory
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->m_free);
+    if (!wait(&sh->m_free, piece & 1)) return false;
+    if (!wide) ++merges;
   }
 }
 
@@ -1312,13 +1331,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
       mbar_init(&sh->v_full[i], 4);
       mbar_init(&sh->v_empty[i], 1);
       mbar_init(&sh->s_full[i], 1);
-      mbar_init(&sh->p_full[i], 4);
+      mbar_init(&sh->p_full[i], 8);
       mbar_init(&sh->d_full[i], 1);
-      mbar_init(&sh->d_empty[i], 17 + kCopiers);  // softmax 8, keys 4, values 4, MMA 1, copies
+      mbar_init(&sh->d_empty[i], 25 + kCopiers);  // softmax 16, keys 4, values 4, MMA 1, copies
     }
-    mbar_init(&sh->q_full, 8);
-    mbar_init(&sh->m_full, 4);
-    mbar_init(&sh->m_free, 4);
+    mbar_init(&sh->q_full, 16);
+    mbar_init(&sh->m_full, 8);
+    mbar_init(&sh->m_free, 16);
+    for (int i = 0; i < 8; ++i) mbar_init(&sh->x_full[i >> 2][i & 3], 2);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh->ring_full[i], 32);
       mbar_init(&sh->ring_empty[i], 2 * C::PARTS);
