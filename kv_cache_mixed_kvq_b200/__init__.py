@@ -124,8 +124,9 @@ def library() -> ctypes.CDLL:
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev_ptr(t: torch.Tensor, name: str) -> int:
@@ -199,7 +200,23 @@ class KVCache:
                    num_pages=num_pages if page_size else 0,
                    block_table=block_table if page_size else None)
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_desc", None)
+
     def desc(self) -> KvqCacheDesc:
+        """The C descriptor; built again when a field or a buffer's address has
+        changed since the last call."""
+        bt = self.block_table
+        at = (self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_params.data_ptr(),
+              self.v_params.data_ptr(), bt.data_ptr() if bt is not None else None)
+        kept = self.__dict__.get("_desc")
+        if kept is None or kept[0] != at:
+            kept = (at, self._build_desc())
+            self.__dict__["_desc"] = kept
+        return kept[1]
+
+    def _build_desc(self) -> KvqCacheDesc:
         flags = (KVQ_FLAG_ROTATE_KEYS if self.rotate_keys else 0) | \
             (KVQ_FLAG_PAGED if self.page_size else 0)
         bt = _dev_ptr(self.block_table, "block_table") if self.block_table is not None else None
@@ -306,7 +323,7 @@ def _on_current(device: torch.device) -> None:
     """The library launches on the current device: its tensors must be there."""
     if device.type != "cuda":
         raise ValueError("the cache must be on a CUDA device")
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on {device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 
@@ -375,9 +392,10 @@ def kvq_plan_append(cache: KVCache, old_lens: torch.Tensor, new_lens: torch.Tens
         users = None
     lib = library()
     E = lib.kvq_slot_map_entries(B, num_tokens)
-    slot_map = torch.empty((E, 4), dtype=torch.int32, device=device)
-    lens = torch.empty(B, dtype=torch.int32, device=device)
-    cu = torch.empty(B + 1, dtype=torch.int32, device=device)
+    # (one allocation: three took half of the call's host time)
+    slot_map, lens, cu = torch.empty(4 * E + 2 * B + 1, dtype=torch.int32,
+                                     device=device).split_with_sizes((4 * E, B, B + 1))
+    slot_map = slot_map.view(E, 4)
     d = cache.desc()
     st = lib.kvq_plan_append(ctypes.byref(d), old, new, num_tokens, users, lens.data_ptr(),
                              cu.data_ptr(), slot_map.data_ptr() if E else None, E,

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   int total = 0;
   if (paged) {
     int mine = 0;
+#pragma unroll 4
     for (int i = lo + 4 * t; i < hi; i += 4 * kPlanThreads) mine += free4(load4(i));
     block_scan(mine, warp_sums, &total);
     if (t == 0) s_free = total;

@@ -2,28 +2,30 @@
 // kvq_dequantize_ragged): packed tokens of rows of any lengths, each 16-position
 // tile that takes tokens named by one entry of the slot map.
 //
-// One CTA handles one entry of one kv head, keys or values.  A thread owns a
-// unit of 8 consecutive elements of one token (one 16-byte load of a 16-bit
-// type), the D/8 units of a row in consecutive lanes.  Bits and group sizes
-// are runtime values (uniform over the launch): a unit's eight codes are built
-// from the same binary32 steps as in quantize.cuh,
+// One CTA handles one entry of one kv head, keys or values.  A thread owns two
+// units of 8 consecutive elements of one token, the D/16 threads of a row in
+// consecutive lanes.  Bits and group sizes are runtime values (uniform over
+// the launch); the codes come from the same binary32 steps as in quantize.cuh,
 //   mn, mx = group min and max (xor-shuffles over the group's lanes);
 //   scale = (mx - mn) / (2^b - 1);  inv = 1 / scale;
 //   code = rint((x - mn) * inv), 0 for a degenerate group,
-// and both layouts keep a unit's codes at one place of a word: element
-// d = 8u + m (unit u, m = 0..7) sits at bit 16 (m mod 2) + b (u mod E) of
+// rint by adding 1.5 * 2^23, whose sum's low mantissa bits are the code.  Both
+// layouts keep a unit's codes at one place of a word: element d = 8u + m
+// (unit u, m = 0..7) sits at bit 16 (m mod 2) + b (u mod E) of
 //   keys:   word u/E of slice m/2 of its row,
 //   values: (position k of the tile) half k mod 2 of word (k/8) W + u/E of
 //           lane 4m + (k mod 8)/2 (bit offset without the 16 (m mod 2)),
 // E = 16/b, so a register per slice holds elements 2c and 2c+1 in its halves,
-// shifted by b (u mod E), and an exclusive or over the E lanes of a word
-// completes it (the fields are disjoint).
+// shifted by b (u mod E); an or over the word's lanes completes it (the
+// fields are disjoint).
 //
 // Bound: HBM traffic for long chunks (2 D es bytes in, D (bk + bv) / 8 + 4
 // (D/Gk + D/Gv) out per token and head), launch latency for single tokens.
 // Whole tiles are assembled in shared memory and leave as 16-byte stores; an
 // edge tile's words go to global memory one by one, so that positions of no
-// entry keep their bytes.
+// entry keep their bytes.  (One unit a thread took 39 us for 8200 tokens of
+// 8 heads, head_dim 128, K4V2: the group's exchanges and quotients are per
+// thread.)
 #include "common.cuh"
 #include "internal.h"
 #include "serve.h"
@@ -71,24 +73,25 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Walsh-Hadamard butterfly h = 1, 2, ..., D/2 of a row whose unit u is in
-// lane u: stages below 8 inside the thread, the others by xor-shuffles.
+// Walsh-Hadamard butterfly h = 1, 2, ..., D/2 of a row whose elements 16 t ..
+// 16 t + 15 are in lane t: stages below 16 inside the thread, the others by
+// xor-shuffles.
 template <int D>
-__device__ __forceinline__ void rotate_units(float (&x)[8], int u) {
+__device__ __forceinline__ void rotate_row(float (&x)[16], int t) {
 #pragma unroll
-  for (int h = 1; h < 8; h *= 2)
+  for (int h = 1; h < 16; h *= 2)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if ((i & h) == 0) {
         const float p = x[i], q = x[i + h];
         x[i] = __fadd_rn(p, q);
         x[i + h] = __fsub_rn(p, q);
       }
 #pragma unroll
-  for (int m = 1; m < D / 8; m *= 2) {
-    const bool upper = (u & m) != 0;
+  for (int m = 1; m < D / 16; m *= 2) {
+    const bool upper = (t & m) != 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float y = __shfl_xor_sync(0xffffffffu, x[i], m);
       x[i] = upper ? __fsub_rn(y, x[i]) : __fadd_rn(x[i], y);
     }
@@ -102,9 +105,16 @@ __device__ __forceinline__ int v_half_offset(int D, int b, int k, int u, int m) 
   return (n / P) * 32 * P + (4 * m + (k & 7) / 2) * P + n % P;
 }
 
+// 16 elements widened to binary32.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
+  Load8<T>::run(p, *reinterpret_cast<float(*)[8]>(x));
+  Load8<T>::run(p + 8, *reinterpret_cast<float(*)[8]>(x + 8));
+}
+
 template <int D, typename TIn, bool ROT>
-__global__ void __launch_bounds__(2 * D) append_ragged_kernel(const RaggedArgs a) {
-  constexpr int U = D / 8;
+__global__ void __launch_bounds__(D) append_ragged_kernel(const RaggedArgs a) {
+  constexpr int U = D / 16;  // threads of a row
   __shared__ __align__(16) uint8_t codes[16 * D];  // a tile at 8 bits
   __shared__ __align__(16) uint32_t params[16 * (D / 32)];
   pdl_wait();
@@ -113,153 +123,167 @@ __global__ void __launch_bounds__(2 * D) append_ragged_kernel(const RaggedArgs a
   if (e.w == 0) return;
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
-  const int b = is_v ? a.c.bits_v : a.c.bits_k, G = is_v ? a.c.group_v : a.c.group;
-  const int u = threadIdx.x % U, r = threadIdx.x / U;  // unit, row of the tile
+  const int b = is_v ? a.c.bits_v : a.c.bits_k, gshift = is_v ? a.c.gshift_v : a.c.gshift_k;
+  const int t = threadIdx.x % U, r = threadIdx.x / U;  // thread of the row, row of the tile
   const int first = e.y & 15;
   const bool full = e.w == 16;
   const bool valid = r >= first && r < first + e.w;
   const size_t row0 =
       (static_cast<size_t>(e.x) * a.c.kv_heads + h) * a.c.block_tokens + (e.y & ~15);
 
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  float x[16];
   if (valid) {
     const TIn* src = static_cast<const TIn*>(is_v ? a.v : a.k) +
                      static_cast<int64_t>(e.z + r - first) * (is_v ? a.v_stride : a.k_stride) +
-                     h * D + 8 * u;
-    Load8<TIn>::run(src, x);
+                     h * D + 16 * t;
+    load16(src, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
   }
-  if (ROT && !is_v) rotate_units<D>(x, u);
+  if (ROT && !is_v) rotate_row<D>(x, t);
 
   float mn = x[0], mx = x[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
+  for (int i = 1; i < 16; ++i) {
     mn = fminf(mn, x[i]);
     mx = fmaxf(mx, x[i]);
   }
-  for (int m = 1; m < G / 8; m <<= 1) {
+  const int lanes = 1 << (gshift - 4);  // threads of a group: 2, 4 or 8
+  for (int m = 1; m < lanes; m <<= 1) {
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, m));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
   }
   mn = (mn == 0.0f) ? 0.0f : mn;  // a zero extreme is stored as +0
   mx = (mx == 0.0f) ? 0.0f : mx;
-  const int levels = (1 << b) - 1;
+  const uint32_t levels = (1u << b) - 1;
   const float scale = __fdiv_rn(__fsub_rn(mx, mn), static_cast<float>(levels));
-  const float inv = __fdiv_rn(1.0f, scale);
+  const float inv = __frcp_rn(scale);
   const bool flat = scale == 0.0f || !isfinite(scale) || !isfinite(inv);
   const float f = flat ? 0.0f : inv, z = flat ? 0.0f : mn;
-  const int shift = b * (u & (16 / b - 1));
+  // word c: elements 2c, 2c + 1 of both units, from bit b (u mod E)
+  const int e1 = 16 / b - 1;
+  const int shift = b * (2 * t & e1);
   uint32_t w[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int lo = __float2int_rn(__fmul_rn(__fsub_rn(x[2 * c], z), f)) & levels;
-    const int hi = __float2int_rn(__fmul_rn(__fsub_rn(x[2 * c + 1], z), f)) & levels;
-    w[c] = static_cast<uint32_t>(lo | (hi << 16)) << shift;
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float d = __fmul_rn(__fsub_rn(x[(i >> 1) * 8 + 2 * c + (i & 1)], z), f);
+      q[i] = __float_as_uint(__fadd_rn(d, 12582912.0f)) & levels;  // 1.5 * 2^23
+    }
+    w[c] = ((q[0] | (q[1] << 16)) | ((q[2] | (q[3] << 16)) << b)) << shift;
   }
-  for (int m = 1; m < 16 / b; m <<= 1) {
+  for (int m = 1; m < 8 / b; m <<= 1) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) w[c] |= __shfl_xor_sync(0xffffffffu, w[c], m);
   }
 
   // the word's first lane stores it; the group's first lane its parameters
-  const bool word_lane = (u & (16 / b - 1)) == 0, group_lane = u % (G / 8) == 0;
+  const bool word_lane = (2 * t & e1) == 0, group_lane = (t & (lanes - 1)) == 0;
   const uint32_t par = pack_half2(__float2half_rn(scale), __float2half_rn(mn));
-  const int row_bytes = D * b / 8, groups = D / G;
-  uint8_t* gcodes = is_v ? a.c.v_codes + row0 * row_bytes  // (a tile has 16 rows' bytes)
-                         : a.c.k_codes + row0 * row_bytes;
+  const int row_bytes = D * b / 8, groups = D >> gshift;
+  uint8_t* gcodes = (is_v ? a.c.v_codes : a.c.k_codes) + row0 * row_bytes;  // (a tile: 16 rows)
   uint32_t* gparams = (is_v ? a.c.v_params : a.c.k_params) + row0 * groups;
   uint8_t* cdst = full ? codes : gcodes;
   uint32_t* pdst = full ? params : gparams;
   if (valid) {
     if (word_lane) {
+      if (!is_v) {
+        uint8_t* row = cdst + r * row_bytes + 4 * (2 * t * b / 16);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (!is_v) {
-          *reinterpret_cast<uint32_t*>(cdst + r * row_bytes + c * (row_bytes / 4) +
-                                       4 * (u * b / 16)) = w[c];
-        } else {
-          *reinterpret_cast<uint16_t*>(cdst + v_half_offset(D, b, r, u, 2 * c)) =
-              static_cast<uint16_t>(w[c]);
-          *reinterpret_cast<uint16_t*>(cdst + v_half_offset(D, b, r, u, 2 * c + 1)) =
-              static_cast<uint16_t>(w[c] >> 16);
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint32_t*>(row + c * (row_bytes / 4)) = w[c];
+      } else {
+        const int P = min(16, D * b / 16);
+        uint8_t* at = cdst + v_half_offset(D, b, r, 2 * t, 0);  // element m: 4 m P bytes on
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          *reinterpret_cast<uint16_t*>(at + 8 * c * P) = static_cast<uint16_t>(w[c]);
+          *reinterpret_cast<uint16_t*>(at + (8 * c + 4) * P) = static_cast<uint16_t>(w[c] >> 16);
         }
       }
     }
-    if (group_lane) pdst[r * groups + u / (G / 8)] = par;
+    if (group_lane) pdst[r * groups + (16 * t >> gshift)] = par;
   }
   if (full) {
     __syncthreads();
-    for (int i = threadIdx.x; i < row_bytes; i += 2 * D)  // 16 rows' bytes / 16
+    for (int i = threadIdx.x; i < row_bytes; i += D)  // 16 rows' bytes / 16
       reinterpret_cast<uint4*>(gcodes)[i] = reinterpret_cast<const uint4*>(codes)[i];
-    for (int i = threadIdx.x; i < 4 * groups; i += 2 * D)
+    for (int i = threadIdx.x; i < 4 * groups; i += D)
       reinterpret_cast<uint4*>(gparams)[i] = reinterpret_cast<const uint4*>(params)[i];
   }
 }
 
 template <int D, typename TOut, bool ROT>
-__global__ void __launch_bounds__(2 * D) dequantize_ragged_kernel(const RaggedArgs a) {
-  constexpr int U = D / 8;
+__global__ void __launch_bounds__(D) dequantize_ragged_kernel(const RaggedArgs a) {
+  constexpr int U = D / 16;
   pdl_wait();
   pdl_trigger();
   const int4 e = load_entry(a, blockIdx.x);
   if (e.w == 0) return;
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
-  const int b = is_v ? a.c.bits_v : a.c.bits_k, G = is_v ? a.c.group_v : a.c.group;
-  const int u = threadIdx.x % U, r = threadIdx.x / U;
+  const int b = is_v ? a.c.bits_v : a.c.bits_k, gshift = is_v ? a.c.gshift_v : a.c.gshift_k;
+  const int t = threadIdx.x % U, r = threadIdx.x / U;
   const int first = e.y & 15;
   const bool valid = r >= first && r < first + e.w;
   const size_t row0 =
       (static_cast<size_t>(e.x) * a.c.kv_heads + h) * a.c.block_tokens + (e.y & ~15);
-  const int row_bytes = D * b / 8, groups = D / G;
-  const int shift = b * (u & (16 / b - 1));
+  const int row_bytes = D * b / 8, groups = D >> gshift;
+  const int shift = b * (2 * t & (16 / b - 1));
   const uint32_t levels = (1u << b) - 1;
-  float x[8];
+  float x[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
   if (valid) {
     const float2 par =
-        unpack_half2((is_v ? a.c.v_params : a.c.k_params)[(row0 + r) * groups + u / (G / 8)]);
-    uint32_t w[4];
+        unpack_half2((is_v ? a.c.v_params : a.c.k_params)[(row0 + r) * groups + (16 * t >> gshift)]);
+    uint32_t w[4];  // elements 2c, 2c + 1 in the halves
     if (!is_v) {
-      const uint8_t* row = a.c.k_codes + (row0 + r) * row_bytes + 4 * (u * b / 16);
+      const uint8_t* row = a.c.k_codes + (row0 + r) * row_bytes + 4 * (2 * t * b / 16);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         w[c] = *reinterpret_cast<const uint32_t*>(row + c * (row_bytes / 4));
     } else {
-      const uint8_t* tile = a.c.v_codes + row0 * row_bytes;
+      const int P = min(16, D * b / 16);
+      const uint8_t* at = a.c.v_codes + row0 * row_bytes + v_half_offset(D, b, r, 2 * t, 0);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint32_t lo =
-            *reinterpret_cast<const uint16_t*>(tile + v_half_offset(D, b, r, u, 2 * c));
-        const uint32_t hi =
-            *reinterpret_cast<const uint16_t*>(tile + v_half_offset(D, b, r, u, 2 * c + 1));
+        const uint32_t lo = *reinterpret_cast<const uint16_t*>(at + 8 * c * P);
+        const uint32_t hi = *reinterpret_cast<const uint16_t*>(at + (8 * c + 4) * P);
         w[c] = lo | (hi << 16);
       }
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      x[2 * c] = fmaf(static_cast<float>((w[c] >> shift) & levels), par.x, par.y);
-      x[2 * c + 1] = fmaf(static_cast<float>((w[c] >> (16 + shift)) & levels), par.x, par.y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // unit i / 2, half i mod 2
+        const uint32_t q = (w[c] >> (shift + (i >> 1) * b + 16 * (i & 1))) & levels;
+        // the code as binary32: its bits in the mantissa of 2^23
+        const float code = __uint_as_float(q | 0x4b000000u) - 8388608.0f;
+        x[(i >> 1) * 8 + 2 * c + (i & 1)] = fmaf(code, par.x, par.y);
+      }
     }
   }
   if (ROT && !is_v) {  // k^ = H (H k^) / D
-    rotate_units<D>(x, u);
+    rotate_row<D>(x, t);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= 1.0f / D;
+    for (int i = 0; i < 16; ++i) x[i] *= 1.0f / D;
   }
   if (valid) {
     TOut* dst = static_cast<TOut*>(const_cast<void*>(is_v ? a.v : a.k)) +
                 static_cast<int64_t>(e.z + r - first) * (is_v ? a.v_stride : a.k_stride) + h * D +
-                8 * u;
-    store8<TOut>(dst, x);
+                16 * t;
+    store8<TOut>(dst, *reinterpret_cast<float(*)[8]>(x));
+    store8<TOut>(dst + 8, *reinterpret_cast<float(*)[8]>(x + 8));
   }
 }
 
 template <int D, typename T>
 cudaError_t launch_typed(const RaggedArgs& a, bool append, cudaStream_t stream) {
-  const dim3 grid(a.num_entries, a.c.kv_heads, 2), block(2 * D);
+  const dim3 grid(a.num_entries, a.c.kv_heads, 2), block(D);
   const bool rot = a.c.rotate_keys;
   if (append)
     return rot ? launch_pdl(append_ragged_kernel<D, T, true>, grid, block, 0, stream, a)
