@@ -62,7 +62,7 @@ namespace kvq {
 namespace chunk {
 
 constexpr int kThreads = 28 * 32;
-constexpr int kWarpsK = 16, kWarpsV = 20, kWarpMma = 24, kWarpList = 25, kWarpCopy = 26;
+constexpr int kWarpUnpack = 16, kWarpMma = 24, kWarpList = 25, kWarpCopy = 26;
 constexpr int kCopiers = 2;       // warps that copy, block by block in turn
 // Registers a thread at launch, and of each warpgroup after the split: 512 x 80
 // + 256 x 64 + 128 x 56 <= 896 x 72.  (Seven warps share an SM quarter's 16384
@@ -712,7 +712,8 @@ template <class C, bool KEYS, int B>
 __device__ __forceinline__ bool unpack_role(const ChunkArgs& a, Shared* sh, uint8_t* tiles,
                                             const uint8_t* ring, const RingLayout& rl,
                                             const Waiter& wait) {
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = ((warp - kWarpUnpack) >> 2) * 2 + (warp & 1);  // of the role's four
   const int blk = w / C::PARTS, part = w % C::PARTS;
   uint64_t* full = KEYS ? sh->k_full : sh->v_full;
   uint64_t* empty = KEYS ? sh->k_empty : sh->v_empty;
@@ -1360,12 +1361,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
   const uint32_t tmem = sh->tmem;
   const Waiter wait{&sh->abort};
 
-  if (warp < kWarpsK) {
+  if (warp < kWarpUnpack) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     softmax_role<C, ROT>(a, sh, smem, tmem, wait);
   } else if (warp < kWarpMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
-    if (warp < kWarpsV) {
+    if ((warp & 2) == 0) {
       uint8_t* tiles = smem + C::SMEM_K;
       if (a.c.bits_k == 2)
         unpack_role<C, true, 2>(a, sh, tiles, ring, rl, wait);
