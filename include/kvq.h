@@ -519,7 +519,17 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  * KVQ_DEVERR_SEQ_LEN; rows whose offsets are not ascending, pass num_tokens
  * or exceed max_q_len are skipped and flag KVQ_DEVERR_BAD_POS.  Block-table
  * entries outside the pool flag KVQ_DEVERR_BAD_PAGE, are not followed, and
- * leave that row's output unspecified.
+ * leave that row's output unspecified.  batch <= 16384, and num_tokens * Hq
+ * and the (query tile, key tile) pairs of a kv head stay below 2^30
+ * (KVQ_ERR_UNSUPPORTED above).
+ *
+ * Kernel launches: one, and a second one that joins partial results when rows
+ * are long enough to be divided; rows of one 16-bit token each go to
+ * kvq_decode_attention().  Arithmetic: products of binary16 operands on the
+ * tensor cores with binary32 sums; a key, value or query is rounded once to
+ * binary16 when the queries are bf16, and held in two binary16 halves (2^-22)
+ * where that would be coarser than the query's type (keys and values for f16,
+ * all operands for f32).  Softmax in binary32.
  */
 int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_stride,
                         int32_t q_dtype, int32_t num_q_heads, int32_t num_tokens,

@@ -74,6 +74,11 @@ int check_chunk(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len, 
   if (c->batch > kChunkRows) return KVQ_ERR_UNSUPPORTED;
   // the (token, query head) rows are counted in 32 bits
   if (static_cast<long long>(num_tokens) * Hq > 0x7fffffffll / 2) return KVQ_ERR_UNSUPPORTED;
+  // and so are a kv head's steps: units of at least 128 rows by tiles
+  const long long units =
+      static_cast<long long>(num_tokens) * (Hq / c->kv_heads) / 128 + std::min(c->batch, num_tokens);
+  const long long tiles = std::min(max_seq_len, c->capacity) / 64 + 1 + kUnitCost;
+  if (units * tiles > 0x7fffffffll / 2) return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;
 }
 

@@ -72,8 +72,8 @@ static_assert(512 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThre
               "more registers than the launch has would never be granted");
 constexpr int kRing = 16;         // ring blocks at most
 constexpr int kBlock = 32;        // positions of a ring block
-constexpr int kSmemMax = 232448;  // shared memory a CTA may have (227 KB)
-constexpr int kHeader = 7 * 1024; // barriers, pieces, merge statistics
+constexpr int kSmemMax = 232448;   // shared memory a CTA may have (227 KB)
+constexpr int kHeader = 7 * 1024;  // barriers, pieces, exchanged maxima and sums
 
 template <int D_, int PIECES_, int NT_>
 struct Cfg {
@@ -569,26 +569,26 @@ __device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const 
       const int je = a.whole_units ? u.steps : max(0, upto - kUnitCost);
       w += upto - within;
       within = 0;
-      if (je > j) {
-      // publish the piece
-      ok = wait(&sh->d_empty[piece & 1], ((piece >> 1) & 1) ^ 1);
-      if (!ok) break;
-      const int t0 = u.wide ? j : min(u.nt, 2 * j), t1 = u.wide ? min(u.nt, je) : min(u.nt, 2 * je);
-      if (lane == 0) {
-        Piece& p = sh->piece[piece & 1];
-        p.valid = 1;
-        p.b = b; p.h = h; p.start = r.start; p.n = r.n; p.len = r.len;
-        p.row0 = u.row0; p.rows = u.rows; p.wide = u.wide; p.lim = u.lim;
-        p.t0 = t0; p.t1 = t1; p.nt0 = u.nt0;
-        p.j0 = j; p.j1 = je; p.begin = j == 0; p.end = je == u.steps;
-        mbar_arrive(&sh->d_full[piece & 1]);
-        if (!(p.begin && p.end)) {
-          int* hd = a.ws_head + (blockIdx.x * 2 + p.begin) * 8;
-          hd[0] = 1; hd[1] = r.start; hd[2] = h; hd[3] = u.row0; hd[4] = u.rows; hd[5] = p.end;
-          headers |= 1u << p.begin;
+      if (je > j) {  // publish the piece
+        ok = wait(&sh->d_empty[piece & 1], ((piece >> 1) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          Piece& p = sh->piece[piece & 1];
+          p.valid = 1;
+          p.b = b; p.h = h; p.start = r.start; p.n = r.n; p.len = r.len;
+          p.row0 = u.row0; p.rows = u.rows; p.wide = u.wide; p.lim = u.lim;
+          p.t0 = u.wide ? j : min(u.nt, 2 * j);
+          p.t1 = u.wide ? min(u.nt, je) : min(u.nt, 2 * je);
+          p.nt0 = u.nt0;
+          p.j0 = j; p.j1 = je; p.begin = j == 0; p.end = je == u.steps;
+          mbar_arrive(&sh->d_full[piece & 1]);
+          if (!(p.begin && p.end)) {
+            int* hd = a.ws_head + (blockIdx.x * 2 + p.begin) * 8;
+            hd[0] = 1; hd[1] = r.start; hd[2] = h; hd[3] = u.row0; hd[4] = u.rows; hd[5] = p.end;
+            headers |= 1u << p.begin;
+          }
         }
-      }
-      ++piece;
+        ++piece;
       }
       if (w < w1 && ++m == mt) {  // the next row with tokens
         m = 0;

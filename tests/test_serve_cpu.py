@@ -124,6 +124,9 @@ def test_chunk_refusals():
     assert _chunk(scale=float("nan")) == BAD
     assert _chunk(_desc(capacity=24)) == BAD
     assert _chunk(tokens=2 ** 28) == UNSUP       # rows past 32 bits
+    assert _chunk(_desc(batch=16385)) == UNSUP
+    # (query tile, key tile) pairs past 32 bits
+    assert _chunk(_desc(capacity=2 ** 26), tokens=2 ** 25, maxlen=2 ** 26) == UNSUP
     assert _chunk(tokens=0, q=None) == OK
 
 

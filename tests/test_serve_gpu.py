@@ -592,6 +592,66 @@ def test_calls_on_another_stream():
     assert_close(out, want, tol)
 
 
+def test_two_calls_at_once():
+    """Two streams, each with its own cache and workspace, many calls each."""
+    def make(seed, dtype):
+        cache, users = make_cache(3, 2, 128, 2048, 4, 2, 64, P=64, spare=1, want=[2000, 300, 77])
+        kd, vd, cu_kv = fill(cache, users, [2000, 300, 77], seed)
+        q = tokens(90, 8, 128, dtype, seed + 5)
+        return cache, q, attention_reference(q, kd, vd, cu_kv, [0, 60, 64, 90], [2000, 300, 77], True,
+                                             0.0, q.dtype)
+
+    cases = [make(1, "bf16"), make(2, "f32")]
+    cu, lens = i32([0, 60, 64, 90]), i32([2000, 300, 77])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[], []]
+    for _ in range(4):
+        for i, (cache, q, _) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(kvq.kvq_chunk_attention(cache, q, cu, lens, 60, 2000))
+    torch.cuda.synchronize()
+    assert kvq.kvq_device_error_flags() == 0
+    for (_, _, (want, tol)), got in zip(cases, outs):
+        for o in got:
+            assert_close(o, want, tol)
+            assert torch.equal(o, got[0])
+
+
+def test_cache_beyond_32_bit_offsets():
+    """A pool whose code arrays pass 4 GiB: its last pages are written, read
+    back and attended like the first ones."""
+    P, pages = 256, 16900
+    free = torch.cuda.mem_get_info()[0]
+    if free < 30 << 30:
+        pytest.skip("not enough device memory")
+    table = torch.tensor([[pages - 1, 3, pages - 2]], dtype=torch.int32)
+    cache = kvq.KVCache.allocate(1, 8, 128, 3 * P, 8, 8, 64, page_size=P, num_pages=pages,
+                                 block_table=table)
+    assert cache.k_codes.numel() > 2 ** 32
+    small = kvq.KVCache.allocate(1, 8, 128, 3 * P, 8, 8, 64)
+    T = 700
+    k, v = tokens(T, 8, 128, "bf16", 1), tokens(T, 8, 128, "bf16", 2)
+    q = tokens(65, 16, 128, "bf16", 3)
+    outs = []
+    for c in (cache, small):
+        users = torch.zeros(pages, dtype=torch.int32, device="cuda") if c.page_size else None
+        if users is not None:
+            users[table[0].long()] = 1  # the pages are the row's already
+        _, _, slots = kvq.kvq_plan_append(small, i32([0]), i32([T]), T)
+        if c.page_size:
+            m = slots.cpu()
+            m[:, 0] = table[0][(m[:, 1] // P).long()] * (m[:, 3] > 0)
+            m[:, 1] %= P
+            slots = m.cuda()
+        kvq.kvq_quantize_append_ragged(c, k, v, slots)
+        a, b = kvq.kvq_dequantize_ragged(c, slots, T, torch.float32)
+        outs.append((a, b, kvq.kvq_chunk_attention(c, q, i32([0, 65]), i32([T]), 65, T)))
+    assert kvq.kvq_device_error_flags() == 0
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
 def test_python_refusals():
     cache, users = make_cache(2, 2, 128, 64, 4, 2, 64, P=32, spare=1, want=[64, 64])
     z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
