@@ -62,9 +62,10 @@ constexpr int unit_rows(int pieces) { return pieces == 3 ? 128 : 256; }
 constexpr int tile_tokens(int pieces, int head_dim, int bits_kv) {
   return pieces == 1 && !(head_dim == 128 && bits_kv == 16) ? 128 : 64;
 }
-// Steps that a unit's queries and output are worth in the division of work (8 to
-// 10 thousand cycles on B200, a step about 5).
-constexpr int kUnitCost = 2;
+// Steps that a unit's queries and output are worth in the division of work (20
+// thousand cycles on B200, a step about 5; ragged prefill 516 us with 2, 488 with 3
+// and 5, verification 100, 98 and 105).
+constexpr int kUnitCost = 3;
 // Batch rows one call takes (their prefix sums lie in the tiles' memory).
 constexpr int kChunkRows = 16384;
 
