@@ -98,11 +98,15 @@ __device__ __forceinline__ void rotate_row(float (&x)[16], int t) {
   }
 }
 
-// Byte offset of a value word's half of element 8u + m, position k, in a tile.
-__device__ __forceinline__ int v_half_offset(int D, int b, int k, int u, int m) {
-  const int N = D * b / 16, P = min(16, N), W = D * b / 128;
-  const int n = 4 * ((k / 8) * W + u * b / 16) + 2 * (k & 1);
-  return (n / P) * 32 * P + (4 * m + (k & 7) / 2) * P + n % P;
+// log2 of the bytes of a format lane's piece, min(16, D b / 16).
+__device__ __forceinline__ int v_piece_shift(int D, int b) { return D * b < 256 ? 3 : 4; }
+
+// Byte offset of a value word's half of element 8u, position k, in a tile;
+// element 8u + m lies 4 m pieces on.
+__device__ __forceinline__ uint32_t v_half_offset(int D, uint32_t b, uint32_t k, uint32_t u) {
+  const int ps = v_piece_shift(D, b);
+  const uint32_t n = 4 * ((k >> 3) * (D * b >> 7) + (u * b >> 4)) + 2 * (k & 1);
+  return ((n >> ps) << (ps + 5)) + (((k & 7) >> 1) << ps) + (n & ((1u << ps) - 1));
 }
 
 // 16 elements widened to binary32.
@@ -124,7 +128,8 @@ __global__ void __launch_bounds__(D) append_ragged_kernel(const RaggedArgs a) {
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const int b = is_v ? a.c.bits_v : a.c.bits_k, gshift = is_v ? a.c.gshift_v : a.c.gshift_k;
-  const int t = threadIdx.x % U, r = threadIdx.x / U;  // thread of the row, row of the tile
+  const uint32_t t = threadIdx.x % U;  // thread of the row
+  const int r = threadIdx.x / U;       // row of the tile
   const int first = e.y & 15;
   const bool full = e.w == 16;
   const bool valid = r >= first && r < first + e.w;
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(D) append_ragged_kernel(const RaggedArgs a) {
   const bool flat = scale == 0.0f || !isfinite(scale) || !isfinite(inv);
   const float f = flat ? 0.0f : inv, z = flat ? 0.0f : mn;
   // word c: elements 2c, 2c + 1 of both units, from bit b (u mod E)
-  const int e1 = 16 / b - 1;
+  const int e1 = b == 2 ? 7 : b == 4 ? 3 : 1;  // E - 1
   const int shift = b * (2 * t & e1);
   uint32_t w[4];
 #pragma unroll
@@ -175,15 +180,15 @@ __global__ void __launch_bounds__(D) append_ragged_kernel(const RaggedArgs a) {
     }
     w[c] = ((q[0] | (q[1] << 16)) | ((q[2] | (q[3] << 16)) << b)) << shift;
   }
-  for (int m = 1; m < 8 / b; m <<= 1) {
+  for (int m = 2; m <= e1; m <<= 1) {  // lanes of a word: (e1 + 1) / 2
 #pragma unroll
-    for (int c = 0; c < 4; ++c) w[c] |= __shfl_xor_sync(0xffffffffu, w[c], m);
+    for (int c = 0; c < 4; ++c) w[c] |= __shfl_xor_sync(0xffffffffu, w[c], m >> 1);
   }
 
   // the word's first lane stores it; the group's first lane its parameters
   const bool word_lane = (2 * t & e1) == 0, group_lane = (t & (lanes - 1)) == 0;
   const uint32_t par = pack_half2(__float2half_rn(scale), __float2half_rn(mn));
-  const int row_bytes = D * b / 8, groups = D >> gshift;
+  const uint32_t row_bytes = D * b >> 3, groups = D >> gshift;
   uint8_t* gcodes = (is_v ? a.c.v_codes : a.c.k_codes) + row0 * row_bytes;  // (a tile: 16 rows)
   uint32_t* gparams = (is_v ? a.c.v_params : a.c.k_params) + row0 * groups;
   uint8_t* cdst = full ? codes : gcodes;
@@ -191,13 +196,13 @@ __global__ void __launch_bounds__(D) append_ragged_kernel(const RaggedArgs a) {
   if (valid) {
     if (word_lane) {
       if (!is_v) {
-        uint8_t* row = cdst + r * row_bytes + 4 * (2 * t * b / 16);
+        uint8_t* row = cdst + r * row_bytes + 4 * (t * b >> 3);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint32_t*>(row + c * (row_bytes / 4)) = w[c];
+          *reinterpret_cast<uint32_t*>(row + c * (row_bytes >> 2)) = w[c];
       } else {
-        const int P = min(16, D * b / 16);
-        uint8_t* at = cdst + v_half_offset(D, b, r, 2 * t, 0);  // element m: 4 m P bytes on
+        const int P = 1 << v_piece_shift(D, b);
+        uint8_t* at = cdst + v_half_offset(D, b, r, 2 * t);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           *reinterpret_cast<uint16_t*>(at + 8 * c * P) = static_cast<uint16_t>(w[c]);
@@ -209,9 +214,9 @@ __global__ void __launch_bounds__(D) append_ragged_kernel(const RaggedArgs a) {
   }
   if (full) {
     __syncthreads();
-    for (int i = threadIdx.x; i < row_bytes; i += D)  // 16 rows' bytes / 16
+    for (uint32_t i = threadIdx.x; i < row_bytes; i += D)  // 16 rows' bytes / 16
       reinterpret_cast<uint4*>(gcodes)[i] = reinterpret_cast<const uint4*>(codes)[i];
-    for (int i = threadIdx.x; i < 4 * groups; i += D)
+    for (uint32_t i = threadIdx.x; i < 4 * groups; i += D)
       reinterpret_cast<uint4*>(gparams)[i] = reinterpret_cast<const uint4*>(params)[i];
   }
 }
@@ -226,13 +231,15 @@ __global__ void __launch_bounds__(D) dequantize_ragged_kernel(const RaggedArgs a
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const int b = is_v ? a.c.bits_v : a.c.bits_k, gshift = is_v ? a.c.gshift_v : a.c.gshift_k;
-  const int t = threadIdx.x % U, r = threadIdx.x / U;
+  const uint32_t t = threadIdx.x % U;  // thread of the row
+  const int r = threadIdx.x / U;       // row of the tile
   const int first = e.y & 15;
   const bool valid = r >= first && r < first + e.w;
   const size_t row0 =
       (static_cast<size_t>(e.x) * a.c.kv_heads + h) * a.c.block_tokens + (e.y & ~15);
-  const int row_bytes = D * b / 8, groups = D >> gshift;
-  const int shift = b * (2 * t & (16 / b - 1));
+  const uint32_t row_bytes = D * b >> 3, groups = D >> gshift;
+  const int e1 = b == 2 ? 7 : b == 4 ? 3 : 1;  // E - 1
+  const int shift = b * (2 * t & e1);
   const uint32_t levels = (1u << b) - 1;
   float x[16];
 #pragma unroll
@@ -242,13 +249,13 @@ __global__ void __launch_bounds__(D) dequantize_ragged_kernel(const RaggedArgs a
         unpack_half2((is_v ? a.c.v_params : a.c.k_params)[(row0 + r) * groups + (16 * t >> gshift)]);
     uint32_t w[4];  // elements 2c, 2c + 1 in the halves
     if (!is_v) {
-      const uint8_t* row = a.c.k_codes + (row0 + r) * row_bytes + 4 * (2 * t * b / 16);
+      const uint8_t* row = a.c.k_codes + (row0 + r) * row_bytes + 4 * (t * b >> 3);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        w[c] = *reinterpret_cast<const uint32_t*>(row + c * (row_bytes / 4));
+        w[c] = *reinterpret_cast<const uint32_t*>(row + c * (row_bytes >> 2));
     } else {
-      const int P = min(16, D * b / 16);
-      const uint8_t* at = a.c.v_codes + row0 * row_bytes + v_half_offset(D, b, r, 2 * t, 0);
+      const int P = 1 << v_piece_shift(D, b);
+      const uint8_t* at = a.c.v_codes + row0 * row_bytes + v_half_offset(D, b, r, 2 * t);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint32_t lo = *reinterpret_cast<const uint16_t*>(at + 8 * c * P);
