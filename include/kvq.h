@@ -417,7 +417,8 @@ int32_t kvq_slot_map_entries(int32_t batch, int32_t num_tokens);
  *                table entries that name each page (0: free); updated.  Rows
  *                that share prefix pages count once each.  NULL without
  *                pages.
- *   lens       : device int32[B], written: the rows' lengths after the call.
+ *   lens       : device int32[B], written: the rows' lengths after the call;
+ *                not the memory of old_lens or new_lens.
  *   cu_tokens  : device int32[B + 1], written: cu_tokens[0] = 0,
  *                cu_tokens[b + 1] = cu_tokens[b] + max(0, new_lens[b] - old_lens[b]).
  *   slot_map   : device int32[num_entries][4], 16-byte aligned, written;
@@ -438,7 +439,7 @@ int32_t kvq_slot_map_entries(int32_t batch, int32_t num_tokens);
  * (KVQ_DEVERR_BAD_POS) or above capacity (KVQ_DEVERR_SEQ_LEN) is refused and
  * counts no tokens.  More tokens than num_tokens flag KVQ_DEVERR_CAPACITY;
  * those past it are in no entry.
- * batch <= 8192 (KVQ_ERR_UNSUPPORTED above).  Calls that update the same
+ * batch <= 8192 and capacity <= 2^30 (KVQ_ERR_UNSUPPORTED above).  Calls that update the same
  * table or pool must be ordered by their streams.
  */
 int kvq_plan_append(const kvq_cache_desc* cache, const int32_t* old_lens,
@@ -519,9 +520,9 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  * KVQ_DEVERR_SEQ_LEN; rows whose offsets are not ascending, pass num_tokens
  * or exceed max_q_len are skipped and flag KVQ_DEVERR_BAD_POS.  Block-table
  * entries outside the pool flag KVQ_DEVERR_BAD_PAGE, are not followed, and
- * leave that row's output unspecified.  batch <= 16384, and num_tokens * Hq
- * and the (query tile, key tile) pairs of a kv head stay below 2^30
- * (KVQ_ERR_UNSUPPORTED above).
+ * leave that row's output unspecified.  batch <= 16384, and lengths,
+ * num_tokens * Hq and the (query tile, key tile) pairs of a kv head stay
+ * within 2^30 (KVQ_ERR_UNSUPPORTED above).
  *
  * Kernel launches: one, and a second one that joins partial results when rows
  * are long enough to be divided; rows of one 16-bit token each go to

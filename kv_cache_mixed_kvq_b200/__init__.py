@@ -204,6 +204,9 @@ class KVCache:
         object.__setattr__(self, name, value)
         self.__dict__.pop("_desc", None)
 
+    def __getstate__(self):  # (copies and pickles build their own descriptor)
+        return {k: v for k, v in self.__dict__.items() if k != "_desc"}
+
     def desc(self) -> KvqCacheDesc:
         """The C descriptor; built again when a field or a buffer's address has
         changed since the last call."""

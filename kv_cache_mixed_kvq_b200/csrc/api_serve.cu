@@ -66,12 +66,16 @@ int ragged_impl(const kvq_cache_desc* cache, const void* k, int64_t k_stride, co
   return to_status(append ? launch_append_ragged(a, s) : launch_dequantize_ragged(a, s));
 }
 
+// Positions are counted in 32 bits, rounded up to tiles and pages.
+constexpr int kMaxLength = 1 << 30;
+
 int check_chunk(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len, int max_seq_len) {
   const int st = check_cache(c);
   if (st != KVQ_OK) return st;
   if (Hq < 1 || Hq % c->kv_heads != 0 || num_tokens < 0 || max_q_len < 0 || max_seq_len < 0)
     return KVQ_ERR_INVALID_ARG;
-  if (c->batch > kChunkRows) return KVQ_ERR_UNSUPPORTED;
+  if (c->batch > kChunkRows || std::min(max_seq_len, c->capacity) > kMaxLength)
+    return KVQ_ERR_UNSUPPORTED;
   // the (token, query head) rows are counted in 32 bits
   if (static_cast<long long>(num_tokens) * Hq > 0x7fffffffll / 2) return KVQ_ERR_UNSUPPORTED;
   // and so are a kv head's steps: units of at least 128 rows by tiles
@@ -138,6 +142,20 @@ bool is_decode(const kvq_cache_desc* c, int num_tokens, int max_q_len) {
   return max_q_len == 1 && num_tokens == c->batch;
 }
 
+// Workspace of a call, whatever its element types (arguments checked).
+size_t chunk_workspace(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len,
+                       int max_seq_len) {
+  size_t need = 0;
+  for (int pieces = 1; pieces <= 3; ++pieces) {
+    ChunkPlan p;
+    if (chunk_plan(c, Hq, num_tokens, max_q_len, max_seq_len, pieces, &p) != KVQ_OK) return 0;
+    need = std::max(need, p.bytes);
+  }
+  if (is_decode(c, num_tokens, max_q_len))
+    need = std::max(need, kvq_decode_workspace_bytes(c, Hq, max_seq_len));
+  return need;
+}
+
 }  // namespace
 
 extern "C" {
@@ -154,10 +172,11 @@ int kvq_plan_append(const kvq_cache_desc* cache, const int32_t* old_lens,
                     kvq_stream_t stream) {
   int st = check_cache(cache);
   if (st != KVQ_OK) return st;
-  if (cache->batch > kPlanRows) return KVQ_ERR_UNSUPPORTED;
+  if (cache->batch > kPlanRows || cache->capacity > kMaxLength) return KVQ_ERR_UNSUPPORTED;
   const bool paged = (cache->flags & KVQ_FLAG_PAGED) != 0;
   if (!old_lens || !new_lens || !lens || !cu_tokens || !aligned(old_lens, 4) ||
       !aligned(new_lens, 4) || !aligned(lens, 4) || !aligned(cu_tokens, 4) || num_tokens < 0 ||
+      lens == old_lens || lens == new_lens ||  // (read again after lens is written)
       num_entries < kvq_slot_map_entries(cache->batch, num_tokens) ||
       (num_entries > 0 && (!slot_map || !aligned(slot_map, 16))) ||
       paged != (page_users != nullptr) || !aligned(page_users, 4))
@@ -201,16 +220,7 @@ int kvq_dequantize_ragged(const kvq_cache_desc* cache, const int32_t* slot_map,
 size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_heads,
                                  int32_t num_tokens, int32_t max_q_len, int32_t max_seq_len) {
   if (check_chunk(cache, num_q_heads, num_tokens, max_q_len, max_seq_len) != KVQ_OK) return 0;
-  size_t need = 0;
-  for (int pieces = 1; pieces <= 3; ++pieces) {
-    ChunkPlan p;
-    if (chunk_plan(cache, num_q_heads, num_tokens, max_q_len, max_seq_len, pieces, &p) != KVQ_OK)
-      return 0;
-    need = std::max(need, p.bytes);
-  }
-  if (is_decode(cache, num_tokens, max_q_len))
-    need = std::max(need, kvq_decode_workspace_bytes(cache, num_q_heads, max_seq_len));
-  return need;
+  return chunk_workspace(cache, num_q_heads, num_tokens, max_q_len, max_seq_len);
 }
 
 int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_stride,
@@ -236,7 +246,9 @@ int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_st
   ChunkPlan p;
   st = chunk_plan(cache, num_q_heads, num_tokens, max_q_len, max_seq_len, pieces, &p);
   if (st != KVQ_OK) return st;
-  if (p.bytes > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes))
+  if (p.bytes > 0 &&
+      (!workspace || !aligned(workspace, 16) ||
+       workspace_bytes < chunk_workspace(cache, num_q_heads, num_tokens, max_q_len, max_seq_len)))
     return KVQ_ERR_WORKSPACE;
   const float scale =
       sm_scale > 0.0f ? sm_scale : 1.0f / sqrtf(static_cast<float>(cache->head_dim));

@@ -56,7 +56,10 @@ def test_plan_refusals():
     assert _plan(users=0x600) == BAD             # user counts without pages
     assert _plan(_desc(**PAGED)) == BAD          # pages without user counts
     assert _plan(_desc(**PAGED), users=0x602) == BAD
+    assert _plan(lens=0x100) == BAD              # lens over old_lens, over new_lens
+    assert _plan(lens=0x200) == BAD
     assert _plan(_desc(batch=8193)) == UNSUP
+    assert _plan(_desc(capacity=2 ** 30 + 16)) == UNSUP
     assert _plan(_desc(head_dim=80)) == UNSUP
     assert _plan(_desc(reserved=1)) == BAD
 
@@ -125,6 +128,7 @@ def test_chunk_refusals():
     assert _chunk(_desc(capacity=24)) == BAD
     assert _chunk(tokens=2 ** 28) == UNSUP       # rows past 32 bits
     assert _chunk(_desc(batch=16385)) == UNSUP
+    assert _chunk(_desc(capacity=2 ** 30 + 16), maxlen=2 ** 30 + 16) == UNSUP
     # (query tile, key tile) pairs past 32 bits
     assert _chunk(_desc(capacity=2 ** 26), tokens=2 ** 25, maxlen=2 ** 26) == UNSUP
     assert _chunk(tokens=0, q=None) == OK
@@ -150,3 +154,16 @@ def test_pools_of_many_pages():
     lib = kvq.library()
     assert lib.kvq_validate_cache(ctypes.byref(_desc(**dict(PAGED, num_pages=200000)))) == OK
     assert lib.kvq_validate_cache(ctypes.byref(_desc(batch=65536))) == UNSUP
+
+
+def test_caches_copy_without_their_descriptor():
+    """The descriptor kept by a cache follows its fields and stays out of copies."""
+    import copy
+    cache = kvq.KVCache(2, 2, 128, 64, 4, 2, 64, *(torch.zeros(16, dtype=torch.uint8)
+                                                   for _ in range(4)))
+    cache.__dict__["_desc"] = ((0,) * 5, kvq.KvqCacheDesc())
+    other = copy.deepcopy(cache)
+    assert "_desc" not in other.__dict__ and other.batch == 2
+    assert other.k_codes.data_ptr() != cache.k_codes.data_ptr()
+    cache.rotate_keys = True
+    assert "_desc" not in cache.__dict__

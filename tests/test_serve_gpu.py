@@ -415,6 +415,60 @@ def test_chunk_device_errors():
     assert flags == kvq.KVQ_DEVERR_BAD_PAGE and torch.equal(out[6:], ok[6:])
 
 
+def test_chunk_workspace():
+    lens = [3000, 40]
+    cache, users = make_cache(2, 2, 128, 4096, 4, 2, 64, P=64, spare=1, want=lens)
+    fill(cache, users, lens, 1)
+    q, cu = tokens(40, 4, 128, "bf16", 2), i32([0, 20, 40])
+    need = kvq.kvq_chunk_workspace_bytes(cache, 4, 40, 20, 3000)
+    assert need > 0
+    for ws in (torch.empty(need - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(need + 16, dtype=torch.uint8, device="cuda")[8:]):
+        with pytest.raises(kvq.KvqError) as e:
+            kvq.kvq_chunk_attention(cache, q, cu, i32(lens), 20, 3000, workspace=ws)
+        assert e.value.status == kvq.KVQ_ERR_WORKSPACE
+    # whatever the workspace holds, and wherever it lies in a larger one
+    big = torch.full((need + 64,), 0xff, dtype=torch.uint8, device="cuda")
+    a = kvq.kvq_chunk_attention(cache, q, cu, i32(lens), 20, 3000, workspace=big[16:16 + need])
+    b = kvq.kvq_chunk_attention(cache, q, cu, i32(lens), 20, 3000)
+    assert torch.equal(a, b) and (big[:16] == 0xff).all() and (big[16 + need:] == 0xff).all()
+
+
+def test_chunk_nothing_cached_and_bounds_of_zero():
+    cache, _ = make_cache(2, 2, 128, 256, 4, 2, 64)
+    q = tokens(5, 4, 128, "f16", 2)
+    out = kvq.kvq_chunk_attention(cache, q, i32([0, 2, 5]), i32([0, 0]), 3, 0)
+    assert kvq.kvq_device_error_flags() == 0 and (out == 0).all()
+    out = torch.full_like(q, 7.0)
+    kvq.kvq_chunk_attention(cache, q, i32([0, 2, 5]), i32([0, 0]), 0, 0, out=out)
+    assert kvq.kvq_device_error_flags() == kvq.KVQ_DEVERR_BAD_POS and (out == 7.0).all()
+
+
+def test_single_tokens_of_strided_queries():
+    lens = [100, 1, 64]
+    cache, users = make_cache(3, 2, 128, 256, 4, 2, 64, P=64, spare=1, want=lens)
+    kd, vd, cu_kv = fill(cache, users, lens, 2)
+    q = tokens(3, 12, 128, "bf16", 5)[:, 4:8]
+    out = kvq.kvq_chunk_attention(cache, q, i32([0, 1, 2, 3]), i32(lens), 1, 100)
+    want, tol = attention_reference(q, kd, vd, cu_kv, [0, 1, 2, 3], lens, True, 0.0, q.dtype)
+    assert_close(out, want, tol)
+
+
+def test_a_cache_whose_fields_change():
+    """The descriptor that a cache keeps follows its fields and buffers."""
+    cache, _ = make_cache(1, 2, 128, 64, 4, 2, 64)
+    k, v = tokens(16, 2, 128, "bf16", 1), tokens(16, 2, 128, "bf16", 2)
+    _, _, slots = kvq.kvq_plan_append(cache, i32([0]), i32([16]), 16)
+    kvq.kvq_quantize_append_ragged(cache, k, v, slots)
+    a, _ = kvq.kvq_dequantize_ragged(cache, slots, 16, torch.float32)
+    cache.k_codes = torch.zeros_like(cache.k_codes)
+    b, _ = kvq.kvq_dequantize_ragged(cache, slots, 16, torch.float32)
+    assert not torch.equal(a, b)
+    cache.rotate_keys = True
+    c, _ = kvq.kvq_dequantize_ragged(cache, slots, 16, torch.float32)
+    assert not torch.equal(b, c)
+
+
 def test_chunk_shared_prefix_pages_and_strided_queries():
     cache, users = make_cache(2, 2, 128, 128, 4, 2, 64, P=32, spare=4, want=[96, 0])
     kd, vd, _ = fill(cache, users, [96, 0], 1)
