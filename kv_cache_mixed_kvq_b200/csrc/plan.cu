@@ -12,7 +12,7 @@
 // so the result does not depend on timing (the returns' atomic decrements
 // commute).
 //
-// Bound: latency, one launch and three barriers, and for a large pool the
+// Bound: latency, one launch and up to three barriers, and for a large pool the
 // read of its user counts (4 bytes a page).  One CTA's loads reach about 100
 // GB/s, so a pool of more than kSmallPool pages is counted by a cluster of 8
 // CTAs (the portable limit), each a contiguous part; the CTAs exchange their
@@ -103,8 +103,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   pdl_wait();
   pdl_trigger();
 
+  // ---- what the step does at all (every CTA finds the same): without growing
+  // rows the pool is not counted, without shrinking ones nothing is returned,
+  // and the barriers between go too
+  bool shrinks = false, grows = false;
+  for (int b = t; b < a.batch; b += kPlanThreads) {
+    const Row r = load_row(a, b);
+    shrinks |= r.n < r.o;
+    grows |= r.n > r.o;
+  }
+  const bool returns = __syncthreads_or(shrinks) && paged;
+  const bool takes = __syncthreads_or(grows) && paged;
+
   // ---- pages of shrinking rows go back to the pool: one warp a row
-  if (paged) {
+  if (returns) {
     for (int b = gtid / 32; b < a.batch; b += gthreads / 32) {
       const Row r = load_row(a, b);
       if (!r.ok || r.n >= r.o) continue;
@@ -121,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         if (bad) flag_error(a.err, KVQ_DEVERR_BAD_PAGE);
       }
     }
-    cluster.sync();
+    if (takes) cluster.sync();
   }
 
   // ---- free pages of this CTA's part (whole vectors of 4)
@@ -142,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   };
   auto free4 = [](int4 u) { return (u.x == 0) + (u.y == 0) + (u.z == 0) + (u.w == 0); };
   int total = 0;
-  if (paged) {
+  if (takes) {
     int mine = 0;
 #pragma unroll 4
     for (int i = lo + 4 * t; i < hi; i += 4 * kPlanThreads) mine += free4(load4(i));
@@ -193,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 
   // ---- free pages before this CTA's part, and in all
   int before = 0, all = 0;
-  if (paged) {
+  if (takes) {
     cluster.sync();
     for (int p = 0; p < parts; ++p) {
       const int f = *cluster.map_shared_rank(&s_free, p);
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 
   // ---- free pages to rows: the page of rank r goes to the row whose needs
   // first reach past r
-  if (paged) {
+  if (takes) {
     for (int i0 = lo; i0 < hi && before < taken; i0 += 4 * kPlanThreads) {
       const int i = i0 + 4 * t;
       const int4 u = load4(i);
