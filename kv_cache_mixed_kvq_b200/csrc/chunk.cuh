@@ -383,54 +383,45 @@ __device__ __forceinline__ int key_chunk_swizzle(int chunks, int r) {
 }
 
 // Keys of one ring block into rows of the K tile: one lane a position (row r
-// of the tile), elements [part * D / PARTS, + D / PARTS).  Straight code: a
-// loop over the words, with its branches and register moves, took half as long
-// again.
+// of the tile), elements [part * D / PARTS, + D / PARTS), 32 at a time in a
+// short loop (see rolled; straight code for all of them was 3 to 7 % slower
+// where few rows wait for the keys, 2 % faster at 2048 tokens).
 template <class C, int B>
 __device__ __forceinline__ void unpack_keys(const uint8_t* codes, const uint32_t* params,
                                             int gshift, int pos, int part, bool live,
                                             uint8_t* tile, int r) {
   constexpr int D = C::D, NS = D / 32 / C::PARTS;  // 32-element spans of this lane
-  constexpr int WORDS = NS * B / 4 > 0 ? NS * B / 4 : 1;  // words of a slice it takes
-  constexpr int LOAD = WORDS < 4 ? WORDS : 4;
+  constexpr int LOAD = B == 8 ? 2 : 1;             // words of a slice in a span
   constexpr int E = 16 / B;
   const int groups = D >> gshift;
-  uint32_t scale2[NS], zero2[NS];
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const uint32_t par = live ? params[pos * groups + ((part * NS + i) * 32 >> gshift)] : 0u;
-    scale2[i] = __byte_perm(par, 0, 0x1010);
-    zero2[i] = __byte_perm(par, 0, 0x3232);
-  }
-  fit_range<B>(scale2, zero2);
   const uint8_t* row = codes + pos * (D * B / 8);
   const int swz = key_chunk_swizzle(D * B / 128, pos) << 4;
-  const int w0 = part * NS * B / 4;                        // first word of a slice
-  const int pre = B == 2 && NS == 1 ? (part & 1) * 8 : 0;  // half a word is this lane's
   uint8_t* dst = tile + r * 128;
   const int rx = (r & 7) << 4;
-#pragma unroll
-  for (int l = 0; l < WORDS / LOAD; ++l) {
+#pragma unroll 1
+  for (int i = 0, n = rolled(NS); i < n; ++i) {
+    const int span = part * NS + i;
     uint32_t w[4][LOAD];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int off = c * (D * B / 32) + 4 * (w0 + l * LOAD);
+      const int off = c * (D * B / 32) + (span * B / 4) * 4;
       load_words<LOAD>(row + (((off & ~15) ^ swz) | (off & 15)), w[c]);
-      if (B == 2 && NS == 1) w[c][0] >>= pre;
+      if (B == 2) w[c][0] >>= (span & 1) * 8;
     }
+    const uint32_t par = live ? params[pos * groups + (32 * span >> gshift)] : 0u;
+    uint32_t scale2[1] = {__byte_perm(par, 0, 0x1010)}, zero2[1] = {__byte_perm(par, 0, 0x3232)};
+    fit_range<B>(scale2, zero2);
+    uint8_t* half = dst + (span >> 1) * (C::NT * 128);  // 64 elements a swizzled row
+    const int x0 = ((span & 1) << 6) ^ rx;
 #pragma unroll
-    for (int i = 0; i < LOAD; ++i) {
+    for (int e = 0; e < 4; ++e) {
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int e = 0; e < (NS * 4 < E ? NS * 4 : E); ++e) {
-        const int uu = (l * LOAD + i) * E + e, u = part * NS * 4 + uu;  // unit of the lane, the row
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          value_pair<C::KP>(code_field<B>(w[c][i], e), scale2[uu / 4], zero2[uu / 4], hi[c], lo[c]);
-        uint8_t* at = dst + (u / 8) * (C::NT * 128) + (((u & 7) << 4) ^ rx);
-        store_chunk(at, hi);
-        if constexpr (C::KP == 2) store_chunk(at + C::KPIECE, lo);
-      }
+      for (int c = 0; c < 4; ++c)
+        value_pair<C::KP>(code_field<B>(w[c][e / E], e % E), scale2[0], zero2[0], hi[c], lo[c]);
+      uint8_t* at = half + (x0 ^ (e << 4));
+      store_chunk(at, hi);
+      if constexpr (C::KP == 2) store_chunk(at + C::KPIECE, lo);
     }
   }
 }
@@ -1103,10 +1094,6 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       s_phase ^= 1;
       tc::fence_after_sync();
       if (works) {
-        // The scores are read twice, for their maximum and for the weights.
-        // (One pass with the weights held in registers until the maximum is
-        // known was slower: its loop, unrolled over the registers, does not
-        // stay in the instruction cache beside the other roles'.)
         const int seen = limit - t * C::NT - half * NH;
         if (__any_sync(0xffffffffu, seen < NH)) {  // masked: -inf in place
 #pragma unroll 1
@@ -1121,23 +1108,21 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
           }
           tc::wait_st();
         }
-        uint32_t s[2][16];  // 16 scores at a time, the next ones on their way
+        // The scores are read twice, for their maximum and for the weights, 16 at
+        // a time in short loops: held in registers, or with the next 16 on their
+        // way, the longer code costs more than it hides.
         float mx;
         {
           float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};  // (a chain each)
-          tc::ld_32x32b<16>(s_tmem, s[0]);
 #pragma unroll 1
-          for (int i = 0, in = rolled(NH / 32); i < in; ++i) {
+          for (int i = 0, in = rolled(NH / 16); i < in; ++i) {
+            uint32_t s[16];
+            tc::ld_32x32b<16>(s_tmem + 16 * i, s);
+            tc::wait_ld(s);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              tc::wait_ld(s[x]);
-              // (the last read wraps round to the first scores, for the weights)
-              tc::ld_32x32b<16>(s_tmem + ((32 * i + 16 * x + 16) & (NH - 1)), s[x ^ 1]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                top[k & 3] = fmaxf(top[k & 3], fmaxf(__uint_as_float(s[x][2 * k]),
-                                                     __uint_as_float(s[x][2 * k + 1])));
-            }
+            for (int k = 0; k < 8; ++k)
+              top[k & 3] = fmaxf(top[k & 3], fmaxf(__uint_as_float(s[2 * k]),
+                                                   __uint_as_float(s[2 * k + 1])));
           }
           float theirs;
           mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
@@ -1168,26 +1153,23 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
         if constexpr (C::PIECES < 3) {
           // (a chunk's weights take columns that were read)
 #pragma unroll 1
-          for (int i = 0, in = rolled(NH / 32); i < in; ++i) {
-            uint32_t p[16];
+          for (int i = 0, in = rolled(NH / 16); i < in; ++i) {
+            uint32_t s[16], p[8];
+            tc::ld_32x32b<16>(s_tmem + 16 * i, s);
+            tc::wait_ld(s);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              tc::wait_ld(s[x]);
-              if (x == 0 || i + 1 < in)
-                tc::ld_32x32b<16>(s_tmem + 32 * i + 16 * x + 16, s[x ^ 1]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                uint32_t none;
-                weights<C::PIECES>(s[x][2 * k], s[x][2 * k + 1], c2, shift2, sum2[k & 1],
-                                   p[8 * x + k], none);
-              }
+            for (int k = 0; k < 8; ++k) {
+              uint32_t none;
+              weights<C::PIECES>(s[2 * k], s[2 * k + 1], c2, shift2, sum2[k & 1], p[k], none);
             }
-            tc::st_32x32b_x16(s_tmem + 16 * i, p);
+            tc::st_32x32b_x8(s_tmem + 8 * i, p);
           }
         } else {
           // two binary16 pieces take a score's column each: all scores are
           // read before the first are written
           static_assert(C::PIECES < 3 || NH == 32, "the scores of half a tile in two loads");
+          uint32_t s[2][16];
+          tc::ld_32x32b<16>(s_tmem, s[0]);
           tc::ld_32x32b<16>(s_tmem + 16, s[1]);
           tc::wait_ld(s[0]);
           tc::wait_ld(s[1]);
