@@ -26,10 +26,12 @@
 //
 // Roles (28 warps, one CTA per SM):
 //   warps 0-15  softmax: two slots of eight warps; two threads a row of a slot
-//   warps 16-19 keys: packed codes from the ring to a K tile (binary16,
-//               128-byte swizzle)
-//   warps 20-23 values: the same to a V tile (rows are elements: K-major along
-//               the positions, which is the order of the packed V tiles)
+//   warps 16-23 unpacking, those of SM quarters 0 and 1 the keys: packed codes
+//               from the ring to a K tile (binary16, 128-byte swizzle), those
+//               of quarters 2 and 3 the values, to a V tile (rows are
+//               elements: K-major along the positions, which is the order of
+//               the packed V tiles).  A quarter that holds the code of one of
+//               them alone was 1 to 6 % faster.
 //   warp 24     issues the MMAs
 //   warp 25     walks the work list and publishes each piece of work
 //   warps 26-27 copy packed codes and parameters, 32 positions at a time, into
@@ -362,12 +364,9 @@ template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   if constexpr (N == 1) {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (N == 2) {
+  } else {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
     w[0] = u.x; w[1] = u.y;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
   }
 }
 
