@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       }
     }
     int sum;
-    const int e = block_scan(tiles, warp_sums, &sum);  // (every s_end of this round was read)
+    const int e = block_scan(tiles, warp_sums, &sum);  // (every s_end of this pass was read)
     if (b < a.batch) s_end[b] = tiles_before + e;
     tiles_before += sum;
   }

@@ -415,6 +415,15 @@ def test_chunk_device_errors():
     assert flags == kvq.KVQ_DEVERR_BAD_PAGE and torch.equal(out[6:], ok[6:])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_chunk_many_rows(dtype):
+    """Thousands of rows, most of them idle."""
+    r = random.Random(3)
+    lens = [r.randint(0, 90) for _ in range(3000)]
+    n_new = [min(n, r.choice([0, 0, 0, 1, 2])) for n in lens]
+    _chunk_case(lens, n_new, 2, 1, 64, (4, 2), 32, 0, 32, False, dtype, True)
+
+
 def test_chunk_workspace():
     lens = [3000, 40]
     cache, users = make_cache(2, 2, 128, 4096, 4, 2, 64, P=64, spare=1, want=lens)
