@@ -25,6 +25,11 @@ chunks, draft tokens, single tokens), packed one after another::
 
 A paged cache (block tables) is allocated with ``page_size``, ``num_pages``
 and an int32 ``block_table`` [batch][capacity / page_size].
+
+With ``stream=`` a call runs on that stream: its results and workspace are
+memory of that stream, and its arguments may be dropped right after the call.
+Ordering it after the work that produces the arguments, and the reader of its
+results after it, is up to the caller, as with any two streams.
 """
 from __future__ import annotations
 
@@ -129,6 +134,30 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _empty(shape, dtype: torch.dtype, device: torch.device,
+           stream: Optional[torch.cuda.Stream], kept: bool = True) -> torch.Tensor:
+    """Memory of the call's own.  It is taken on the stream that the call runs
+    on: another stream's free memory may still be in use there, and what the
+    call drops could be given out again while its kernels use it.  A result
+    (kept) is also marked as used by the caller's stream, which will read it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if kept:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _used_on(stream: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+    """Marks tensors of other streams as used by the call's, so that their
+    memory is not given out again before the call is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _dev_ptr(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -219,6 +248,10 @@ class KVCache:
             self.__dict__["_desc"] = kept
         return kept[1]
 
+    def _buffers(self):
+        """The cache's tensors (without pages the last one is None)."""
+        return self.k_codes, self.v_codes, self.k_params, self.v_params, self.block_table
+
     def _build_desc(self) -> KvqCacheDesc:
         flags = (KVQ_FLAG_ROTATE_KEYS if self.rotate_keys else 0) | \
             (KVQ_FLAG_PAGED if self.page_size else 0)
@@ -247,6 +280,7 @@ def kvq_quantize_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: t
                                        _DTYPE[k.dtype], _dev_ptr(pos, "pos"), k.shape[2],
                                        _stream_ptr(stream))
     _check(st, "kvq_quantize_append")
+    _used_on(stream, k, v, pos, *cache._buffers())
 
 
 def kvq_decode_workspace_bytes(cache: KVCache, num_q_heads: int, max_seq_len: int) -> int:
@@ -271,13 +305,13 @@ def kvq_decode_attention(cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor
     if seq_lens.dtype != torch.int32:
         raise ValueError("seq_lens must be int32")
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     d = cache.desc()
     lib = library()
     if workspace is None:  # (a given workspace is checked by the library itself)
         need = int(lib.kvq_decode_workspace_bytes(ctypes.byref(d), q.shape[1], max_seq_len))
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _empty(need, torch.uint8, q.device, stream, kept=False)
     ws_ptr = _dev_ptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib.kvq_decode_attention(ctypes.byref(d), _dev_ptr(q, "q"), _DTYPE[q.dtype], q.shape[1],
@@ -285,6 +319,7 @@ def kvq_decode_attention(cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor
                                   float(sm_scale), _dev_ptr(out, "out"), _DTYPE[out.dtype],
                                   ws_ptr, ws_bytes, _stream_ptr(stream))
     _check(st, "kvq_decode_attention")
+    _used_on(stream, q, seq_lens, out, workspace, *cache._buffers())
     return out
 
 
@@ -303,13 +338,13 @@ def kvq_append_decode_attention(cache: KVCache, k_new: torch.Tensor, v_new: torc
     if seq_lens.dtype != torch.int32:
         raise ValueError("seq_lens must be int32")
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     d = cache.desc()
     lib = library()
     if workspace is None:  # (a given workspace is checked by the library itself)
         need = int(lib.kvq_decode_workspace_bytes(ctypes.byref(d), q.shape[1], max_seq_len))
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _empty(need, torch.uint8, q.device, stream, kept=False)
     ws_ptr = _dev_ptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib.kvq_append_decode_attention(
@@ -318,6 +353,7 @@ def kvq_append_decode_attention(cache: KVCache, k_new: torch.Tensor, v_new: torc
         _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len), float(sm_scale), _dev_ptr(out, "out"),
         _DTYPE[out.dtype], ws_ptr, ws_bytes, _stream_ptr(stream))
     _check(st, "kvq_append_decode_attention")
+    _used_on(stream, k_new, v_new, q, seq_lens, out, workspace, *cache._buffers())
     return out
 
 
@@ -396,14 +432,15 @@ def kvq_plan_append(cache: KVCache, old_lens: torch.Tensor, new_lens: torch.Tens
     lib = library()
     E = lib.kvq_slot_map_entries(B, num_tokens)
     # (one allocation: three took half of the call's host time)
-    slot_map, lens, cu = torch.empty(4 * E + 2 * B + 1, dtype=torch.int32,
-                                     device=device).split_with_sizes((4 * E, B, B + 1))
+    slot_map, lens, cu = _empty(4 * E + 2 * B + 1, torch.int32, device,
+                                stream).split_with_sizes((4 * E, B, B + 1))
     slot_map = slot_map.view(E, 4)
     d = cache.desc()
     st = lib.kvq_plan_append(ctypes.byref(d), old, new, num_tokens, users, lens.data_ptr(),
                              cu.data_ptr(), slot_map.data_ptr() if E else None, E,
                              _stream_ptr(stream))
     _check(st, "kvq_plan_append")
+    _used_on(stream, old_lens, new_lens, page_users, cache.block_table)
     return lens, cu, slot_map
 
 
@@ -423,6 +460,7 @@ def kvq_quantize_append_ragged(cache: KVCache, k: torch.Tensor, v: torch.Tensor,
                                               k.shape[0], sp, slot_map.shape[0],
                                               _stream_ptr(stream))
     _check(st, "kvq_quantize_append_ragged")
+    _used_on(stream, k, v, slot_map, *cache._buffers())
 
 
 def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: int,
@@ -441,8 +479,8 @@ def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: in
     if k_out is None:
         if dtype not in _DTYPE:
             raise ValueError("dtype must be float32, bfloat16 or float16")
-        k_out = torch.empty(shape, dtype=dtype, device=device)
-        v_out = torch.empty(shape, dtype=dtype, device=device)
+        k_out = _empty(shape, dtype, device, stream)
+        v_out = _empty(shape, dtype, device, stream)
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if tuple(t.shape) != shape or t.dtype not in _DTYPE or t.dtype != k_out.dtype or \
                 t.device != device:
@@ -453,6 +491,7 @@ def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: in
                                          _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"),
                                          _DTYPE[k_out.dtype], num_tokens, _stream_ptr(stream))
     _check(st, "kvq_dequantize_ragged")
+    _used_on(stream, slot_map, k_out, v_out, *cache._buffers())
     return k_out, v_out
 
 
@@ -480,7 +519,7 @@ def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor
     cu = _int32(cu_tokens, cache.batch + 1, "cu_tokens", device)
     lens = _int32(seq_lens, cache.batch, "seq_lens", device)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=device)
+        out = _empty((T, Hq, D), out_dtype or q.dtype, device, stream)
     elif out.shape != q.shape or out.dtype not in _DTYPE or out.device != device:
         raise ValueError("out must be of q's shape, on the cache's device")
     d = cache.desc()
@@ -488,7 +527,7 @@ def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor
     if workspace is None:  # (a given workspace is checked by the library itself)
         need = lib.kvq_chunk_workspace_bytes(ctypes.byref(d), Hq, T, max_q_len, max_seq_len)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            workspace = _empty(need, torch.uint8, device, stream, kept=False)
     ws_ptr = _dev_ptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib.kvq_chunk_attention(ctypes.byref(d), qp, qs, _DTYPE[q.dtype], Hq, T, cu, lens,
@@ -496,6 +535,7 @@ def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor
                                  _dev_ptr(out, "out"), _DTYPE[out.dtype], ws_ptr, ws_bytes,
                                  _stream_ptr(stream))
     _check(st, "kvq_chunk_attention")
+    _used_on(stream, q, cu_tokens, seq_lens, out, workspace, *cache._buffers())
     return out
 
 

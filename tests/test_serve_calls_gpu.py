@@ -1,0 +1,109 @@
+"""GPU tests of how the serving step is called: on which stream a call's
+memory lives, from several host threads, with padded batches, with values that
+are not finite, and with waits that run out."""
+import pytest
+import torch
+
+import kv_cache_mixed_kvq_b200 as kvq
+from tests.serve_util import (assert_close, attention_reference, fill, i32, make_cache, tokens)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- streams
+def _stream_of(t):
+    """Raw stream that the caching allocator took a tensor's memory on."""
+    at = t.data_ptr()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= at < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def test_results_and_workspace_belong_to_the_call_stream(monkeypatch):
+    lens = [3000, 40]
+    cache, users = make_cache(2, 2, 128, 4096, 4, 2, 64, P=64, spare=4, want=lens)
+    fill(cache, users, lens, 1)
+    q, q2 = tokens(40, 4, 128, "bf16", 2), tokens(2, 4, 128, "bf16", 2)
+    k, v = tokens(2, 2, 128, "bf16", 3), tokens(2, 2, 128, "bf16", 4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    made = []
+    empty = torch.empty
+
+    def logged(*a, **kw):
+        made.append(empty(*a, **kw))
+        return made[-1]
+
+    monkeypatch.setattr(torch, "empty", logged)
+    with torch.cuda.stream(s):
+        old, new, cu, at = i32(lens), i32([3001, 41]), i32([0, 20, 40]), i32([3000, 40])
+    plan = kvq.kvq_plan_append(cache, old, new, 2, users, stream=s)
+    kvq.kvq_quantize_append_ragged(cache, k, v, plan[2], stream=s)
+    results = [*plan, *kvq.kvq_dequantize_ragged(cache, plan[2], 2, stream=s),
+               kvq.kvq_chunk_attention(cache, q, cu, at, 20, 3000, stream=s),
+               kvq.kvq_decode_attention(cache, q2, at, 3000, stream=s)]
+    kn = k.view(2, 2, 1, 128)
+    results.append(kvq.kvq_append_decode_attention(cache, kn, kn, q2, plan[0], 3001, stream=s))
+    monkeypatch.undo()
+    assert len(made) >= 9  # (results and three workspaces)
+    for t in made + results:
+        assert _stream_of(t) == s.cuda_stream
+    s.synchronize()
+    assert kvq.kvq_device_error_flags() == 0
+
+
+def test_overlapping_calls_by_the_stream_argument():
+    """Calls on two streams from one current stream, which takes and drops
+    memory of the workspaces' size in between: each has its own memory."""
+    lens, cu = [2000, 300, 77], i32([0, 60, 64, 90])
+
+    def make(seed, dtype):
+        cache, users = make_cache(3, 2, 128, 2048, 4, 2, 64, P=64, spare=1, want=lens)
+        kd, vd, cu_kv = fill(cache, users, lens, seed)
+        q = tokens(90, 8, 128, dtype, seed + 5)
+        want = attention_reference(q, kd, vd, cu_kv, [0, 60, 64, 90], lens, True, 0.0, q.dtype)
+        return cache, q, want
+
+    cases = [make(1, "bf16"), make(2, "f32")]
+    need = max(kvq.kvq_chunk_workspace_bytes(c, 8, 90, 60, 2000) for c, _, _ in cases)
+    assert need > 0
+    at = i32(lens)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[], []]
+    for _ in range(6):
+        for i, (cache, q, _) in enumerate(cases):
+            outs[i].append(kvq.kvq_chunk_attention(cache, q, cu, at, 60, 2000, stream=streams[i]))
+            torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert kvq.kvq_device_error_flags() == 0
+    for (_, _, (want, tol)), got in zip(cases, outs):
+        for o in got:
+            assert_close(o, want, tol)
+            assert torch.equal(o, got[0])
+
+
+def test_arguments_may_be_dropped_after_the_call():
+    """Memory of the current stream that a call on another one still reads is
+    not given out again."""
+    cache, _ = make_cache(1, 2, 128, 256, 4, 2, 64)
+    slots = kvq.kvq_plan_append(cache, i32([0]), i32([200]), 200)[2]
+    k, v = tokens(200, 2, 128, "bf16", 1), tokens(200, 2, 128, "bf16", 2)
+    kvq.kvq_quantize_append_ragged(cache, k, v, slots)
+    want = [t.clone() for t in (cache.k_codes, cache.v_codes)]
+    for t in (cache.k_codes, cache.v_codes):
+        t.zero_()
+    s = torch.cuda.Stream()
+    k2, v2 = k.clone(), v.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # some 10 ms before the call's turn
+    kvq.kvq_quantize_append_ragged(cache, k2, v2, slots, stream=s)
+    size = k2.numel()
+    del k2, v2
+    for _ in range(4):
+        torch.full((size,), 9.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k_codes, want[0]) and torch.equal(cache.v_codes, want[1])
