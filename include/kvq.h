@@ -496,7 +496,9 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  *   s_t = sm_scale * sum_d q_d * k^_{t,d},   o_d = sum_t softmax(s)_t * v^_{t,d}
  * where query i of the n_b queries of row b attends to the positions
  *   t in [0, seq_lens[b] - n_b + i]  (causal != 0), or [0, seq_lens[b]).
- * A query that sees no position yields o = 0.
+ * A query that sees no position yields o = 0.  NaN and infinities of a query,
+ * or of the parameters of a position that it sees, make its output NaN (or
+ * infinite) as the formula does; they are not flagged.
  *
  *   q           : device, token t of query head hq at t * q_stride + hq * D,
  *                 q_dtype, 16-byte aligned; q_stride >= Hq * D, a multiple of

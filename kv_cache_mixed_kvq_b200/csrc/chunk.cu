@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const ChunkArgs a, int gri
   pdl_trigger();
   const int* hd = a.ws_head + (blockIdx.x * 2 + 1) * 8;
   if (hd[0] == 0 || hd[5] != 0) return;
-  const int start = hd[1], h = hd[2], row0 = hd[3], rows = hd[4];
+  const int start = hd[1], h = hd[2], row0 = hd[3], rows = hd[4], n = hd[6], len = hd[7];
   for (int i = warp; i < kCombineRows; i += 4) {
     const int r = blockIdx.y * kCombineRows + i;
     if (r >= rows) return;
@@ -44,12 +44,13 @@ __global__ void __launch_bounds__(128) combine_kernel(const ChunkArgs a, int gri
       for (int k = 0; k < N; ++k) o[k] = o[k] * f + src[k] * g;
       if (a.ws_head[place * 8 + 5] != 0) break;
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const int br = row0 + r;
+    const bool nothing = chunk::limit_of(a, n, len, br) <= 0;  // no position is seen: 0
+    const float inv = 1.0f / l;
     const size_t orow =
         (static_cast<size_t>(start + br / a.gq) * a.q_heads + h * a.gq + br % a.gq) * D + lane * N;
 #pragma unroll
-    for (int k = 0; k < N; ++k) store_out(a.out, a.out_dtype, orow + k, l > 0.0f ? o[k] * inv : 0.0f);
+    for (int k = 0; k < N; ++k) store_out(a.out, a.out_dtype, orow + k, nothing ? 0.0f : o[k] * inv);
   }
 }
 

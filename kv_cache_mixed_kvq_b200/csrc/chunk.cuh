@@ -590,6 +590,7 @@ __device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const 
           if (!(p.begin && p.end)) {
             int* hd = a.ws_head + (blockIdx.x * 2 + p.begin) * 8;
             hd[0] = 1; hd[1] = r.start; hd[2] = h; hd[3] = u.row0; hd[4] = u.rows; hd[5] = p.end;
+            hd[6] = r.n; hd[7] = r.len;
             headers |= 1u << p.begin;
           }
         }
@@ -1231,8 +1232,11 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       }
     }
     if ((wide || slot == 0) && works) {
+      // A row that sees no position yields 0.  Any other sum is divided by, so
+      // that NaN, and scores of -inf alone, come out as the quotient's NaN.
+      const bool nothing = whole && limit <= 0;
       if (whole) {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // (0: no position is seen)
+        const float inv = nothing ? 0.0f : 1.0f / l;
         f0 *= inv;
         f1 *= inv;
       }
@@ -1249,7 +1253,6 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       // time, so that a store covers whole sectors of many rows.
       uint8_t* stage = smem + slot * C::QTILE + (quarter * 2 + half) * (C::QTILE / 8);
       const uint32_t rows_valid = __ballot_sync(0xffffffffu, valid);
-      const bool nothing = whole && !(l > 0.0f);
 #pragma unroll 1
       for (int i = 0, in = rolled(DH / 16); i < in; ++i) {
         uint32_t o[16];
@@ -1265,7 +1268,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
         for (int k = 0; k < 2; ++k) {
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = nothing ? 0.0f : __uint_as_float(o[8 * k + e]) * f0;
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * k + e]) * f0;
           if (other) {
             const float4 y = merge[(4 * i + 2 * k) ^ (r & 7)];
             const float4 z = merge[(4 * i + 2 * k + 1) ^ (r & 7)];
@@ -1274,6 +1277,8 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
             x[4] = fmaf(z.x, f1, x[4]); x[5] = fmaf(z.y, f1, x[5]);
             x[6] = fmaf(z.z, f1, x[6]); x[7] = fmaf(z.w, f1, x[7]);
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = nothing ? 0.0f : x[e];
           if (wide) {  // rows of 64 bytes; chunk c of row r at c ^ (r / 2 mod 4)
             const int sw = (lane >> 1) & 3;
             if (es == 4) {

@@ -107,3 +107,65 @@ def test_arguments_may_be_dropped_after_the_call():
         torch.full((size,), 9.0, dtype=torch.bfloat16, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(cache.k_codes, want[0]) and torch.equal(cache.v_codes, want[1])
+
+
+# ------------------------------------------------- values that are not finite
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rot", [False, True])
+@pytest.mark.parametrize("lens,n_new", [([150, 70], [40, 3]), ([300], [200]),
+                                        ([3000, 40], [3, 40]), ([4000], [300])])
+def test_query_that_is_not_finite(lens, n_new, rot, dtype):
+    """NaN in its own rows of the output, whole units (narrow and wide) and
+    divided ones; the other rows as ever."""
+    cache, users = make_cache(len(lens), 2, 128, 4096, 4, 2, 64, 0, rot, 64, 3, want=lens)
+    kd, vd, cu_kv = fill(cache, users, lens, 1)
+    cu = [0]
+    for n in n_new:
+        cu.append(cu[-1] + n)
+    q = tokens(cu[-1], 8, 128, dtype, 9)
+    want, tol = attention_reference(q, kd, vd, cu_kv, cu, lens, True, 0.0, q.dtype, rot)
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    for t, h, d, x in ((0, 0, 5, NAN), (1, 7, 0, INF), (cu[-1] - 1, 3, 127, -INF),
+                       (cu[-1] // 2, 4, 64, NAN)):
+        q[t, h, d] = x
+        bad[t, h] = True
+    q[2, 1] = NAN
+    bad[2, 1] = True
+    out = kvq.kvq_chunk_attention(cache, q, i32(cu), i32(lens), max(n_new), max(lens))
+    assert kvq.kvq_device_error_flags() == 0
+    assert torch.isnan(out[bad]).all()
+    assert_close(out[~bad], want[~bad], tol[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("L,n,t", [(200, 60, 150), (3000, 4, 2997), (3000, 4, 17), (700, 300, 640)])
+def test_visible_key_that_is_not_finite(L, n, t, dtype):
+    """A NaN scale of a key reaches the queries that see it, and no other."""
+    cache, _ = make_cache(1, 2, 128, 4096, 4, 2, 64)
+    kd, vd, cu_kv = fill(cache, None, [L], 1)
+    cache.k_params.view(torch.float16).view(2, 4096, 2, 2)[1, t, 0, 0] = NAN
+    q = tokens(n, 8, 128, dtype, 9)
+    want, tol = attention_reference(q, kd, vd, cu_kv, [0, n], [L], True, 0.0, q.dtype)
+    out = kvq.kvq_chunk_attention(cache, q, i32([0, n]), i32([L]), n, L)
+    bad = torch.zeros(n, 8, dtype=torch.bool, device="cuda")
+    bad[max(0, t - (L - n)):, 4:] = True
+    assert torch.isnan(out[bad]).all()
+    assert_close(out[~bad], want[~bad], tol[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("L", [1, 1000])
+def test_scores_of_minus_infinity_alone(L, dtype):
+    """0 / 0, not the output of a query that sees nothing."""
+    cache, _ = make_cache(1, 1, 128, 1024, 4, 2, 64)
+    fill(cache, None, [L], 1)
+    par = cache.k_params.view(torch.float16).view(1024, 2, 2)
+    par[:, :, 0], par[:, :, 1] = 0.0, -INF
+    q = tokens(2, 1, 128, dtype, 9).abs() + 0.5
+    out = kvq.kvq_chunk_attention(cache, q, i32([0, 2]), i32([L]), 2, L, causal=False)
+    assert torch.isnan(out).all()
+    none = kvq.kvq_chunk_attention(cache, q, i32([0, 2]), i32([0]), 2, L, causal=False)
+    assert (none == 0).all()
