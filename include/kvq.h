@@ -420,7 +420,8 @@ int32_t kvq_slot_map_entries(int32_t batch, int32_t num_tokens);
  *   lens       : device int32[B], written: the rows' lengths after the call;
  *                not the memory of old_lens or new_lens.
  *   cu_tokens  : device int32[B + 1], written: cu_tokens[0] = 0,
- *                cu_tokens[b + 1] = cu_tokens[b] + max(0, new_lens[b] - old_lens[b]).
+ *                cu_tokens[b + 1] = cu_tokens[b] + max(0, new_lens[b] - old_lens[b]),
+ *                at most 2^31 - 1.
  *   slot_map   : device int32[num_entries][4], 16-byte aligned, written;
  *                num_entries >= kvq_slot_map_entries(B, num_tokens).  Entries
  *                in row order, positions ascending; the unused last ones are

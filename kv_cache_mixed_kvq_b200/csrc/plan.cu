@@ -38,13 +38,21 @@ constexpr int kPlanCluster = 8;
 // this many user counts.
 constexpr int kSmallPool = 8192;
 
-// Inclusive prefix sum over the CTA's threads; *total: the CTA's sum.
+// Sum of two counts, at most 2^31 - 1: rows may ask for more pages, tiles or
+// tokens than 32 bits count.  Ascending prefix sums stay ascending, and a sum
+// that was cut is more than any pool, map or tensor holds.
+__device__ __forceinline__ int sat_add(int x, int y) {
+  return static_cast<int>(min(static_cast<uint32_t>(x) + static_cast<uint32_t>(y), 0x7fffffffu));
+}
+
+// Inclusive prefix sum (saturating) over the CTA's threads of counts >= 0;
+// *total: the CTA's sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, v, m);
-    if (lane >= m) v += u;
+    if (lane >= m) v = sat_add(v, u);
   }
   __syncthreads();  // the last scan's sums have been read
   if (lane == 31) warp_sums[warp] = v;
@@ -53,11 +61,11 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, s, m);
-    if (lane >= m) s += u;
+    if (lane >= m) s = sat_add(s, u);
   }
   *total = __shfl_sync(0xffffffffu, s, 31);
   const int before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
-  return v + (warp > 0 ? before : 0);
+  return sat_add(v, warp > 0 ? before : 0);
 }
 
 // First index in [0, n) whose (ascending) value exceeds x; n if none does.
@@ -87,6 +95,12 @@ __device__ __forceinline__ Row load_row(const PlanArgs& a, int b) {
     r.n = r.o;
   }
   return r;
+}
+
+// Pages that a growing row takes.
+__device__ __forceinline__ int pages_of(const PlanArgs& a, const Row& r) {
+  const int P1 = (1 << a.page_shift) - 1;
+  return ((r.n + P1) >> a.page_shift) - ((r.o + P1) >> a.page_shift);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
@@ -178,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       if (r.n > r.o) {
         n_new = r.n - r.o;
         if (paged) {
-          need = ((r.n + P1) >> a.page_shift) - ((r.o + P1) >> a.page_shift);
+          need = pages_of(a, r);
           if ((r.o & P1) != 0) {  // its last page takes tokens: it must be this row's alone
             const int page =
                 a.table[static_cast<size_t>(b) * a.pages_per_seq + (r.o >> a.page_shift)];
@@ -196,11 +210,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     }
     int sum;
     const int u = block_scan(need, warp_sums, &sum);
-    if (b < a.batch) s_upto[b] = upto + u;
-    upto += sum;
+    if (b < a.batch) s_upto[b] = sat_add(upto, u);
+    upto = sat_add(upto, sum);
     const int c = block_scan(n_new, warp_sums, &sum);
-    if (b < a.batch) s_cu[b] = tokens + c;
-    tokens += sum;
+    if (b < a.batch) s_cu[b] = sat_add(tokens, c);
+    tokens = sat_add(tokens, sum);
   }
   if (tokens > a.num_tokens && gtid == 0) flag_error(a.err, KVQ_DEVERR_CAPACITY);
   __syncthreads();
@@ -225,8 +239,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     if (b < a.batch) {
       const Row r = load_row(a, b);
       bool refused = s_end[b] != 0;
-      const int need = s_upto[b] - (b > 0 ? s_upto[b - 1] : 0);
-      if (need > 0) {
+      if (paged && !refused && r.n > r.o && pages_of(a, r) > 0) {
         if (s_upto[b] > all) {
           refused = true;
           if (rank == 0) flag_error(a.err, KVQ_DEVERR_NO_PAGE);
@@ -243,8 +256,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     }
     int sum;
     const int e = block_scan(tiles, warp_sums, &sum);  // (every s_end of this pass was read)
-    if (b < a.batch) s_end[b] = tiles_before + e;
-    tiles_before += sum;
+    if (b < a.batch) s_end[b] = sat_add(tiles_before, e);
+    tiles_before = sat_add(tiles_before, sum);
   }
   taken = __reduce_max_sync(0xffffffffu, taken);
   __syncthreads();
@@ -285,9 +298,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     const int b = first_above(s_end, a.batch, e);
     if (b < a.batch) {
       const Row r = load_row(a, b);
-      const int tile = (r.n + 15) / 16 - (s_end[b] - e);
+      const int tile = r.o / 16 + (e - (b > 0 ? s_end[b - 1] : 0));
       const int first = max(16 * tile, r.o), last = min(16 * tile + 16, r.n);
-      const int token = s_cu[b] - (r.n - r.o) + (first - r.o);
+      const int token = sat_add(b > 0 ? s_cu[b - 1] : 0, first - r.o);
       int block = b;
       bool ok = true;
       if (paged) {

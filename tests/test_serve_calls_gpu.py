@@ -169,3 +169,61 @@ def test_scores_of_minus_infinity_alone(L, dtype):
     assert torch.isnan(out).all()
     none = kvq.kvq_chunk_attention(cache, q, i32([0, 2]), i32([0]), 2, L, causal=False)
     assert (none == 0).all()
+
+
+# ------------------------------------------------------- sums past 32 bits
+def _plan_only(B, cap, P=0, pages=0, table=None):
+    """A cache for planning alone, which touches no codes or parameters."""
+    bufs = [torch.zeros(64, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    return kvq.KVCache(B, 1, 64, cap, 2, 2, 64, *bufs, page_size=P, num_pages=pages,
+                       block_table=table)
+
+
+def _summed(new):
+    cu = [0]
+    for n in new:
+        cu.append(min(cu[-1] + n, 2 ** 31 - 1))
+    return cu
+
+
+def test_plan_of_more_tokens_and_tiles_than_32_bits_count():
+    new = [70] + [2 ** 30] * 40 + [9]
+    lens, cu, m = kvq.kvq_plan_append(_plan_only(42, 2 ** 30), i32([0] * 42), i32(new), 100)
+    assert kvq.kvq_device_error_flags() == kvq.KVQ_DEVERR_CAPACITY
+    assert lens.tolist() == new and cu.tolist() == _summed(new)
+    got = [e for e in m.tolist() if e[3]]
+    assert got == [[0, 16 * i, 16 * i, min(16, 70 - 16 * i)] for i in range(5)] + \
+        [[1, 0, 70, 16], [1, 16, 86, 14]]
+
+
+def test_plan_of_refused_tokens_past_32_bits():
+    """Rows that the pool cannot serve keep their place in cu_tokens."""
+    P, B = 2 ** 20, 4
+    table = torch.full((B, 1024), -1, dtype=torch.int32, device="cuda")
+    users = torch.zeros(3, dtype=torch.int32, device="cuda")
+    new = [2 ** 30, 2 ** 30, 2 ** 30, 5]
+    lens, cu, m = kvq.kvq_plan_append(_plan_only(B, 2 ** 30, P, 3, table), i32([0] * B), i32(new),
+                                      5, users)
+    assert kvq.kvq_device_error_flags() == kvq.KVQ_DEVERR_CAPACITY | kvq.KVQ_DEVERR_NO_PAGE
+    assert lens.tolist() == [0] * B and cu.tolist() == _summed(new)
+    assert (m == 0).all() and (users == 0).all() and (table == -1).all()
+
+
+@pytest.mark.parametrize("pages", [1000, 20000])
+def test_plan_of_more_pages_than_32_bits_count(pages):
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough device memory")
+    B, P, cap = 8192, 32, 2 ** 24
+    table = torch.full((B, cap // P), -1, dtype=torch.int32, device="cuda")
+    users = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    users[::3] = 1
+    new = [150, 0, 40] + [cap] * (B - 4) + [33]  # (the last row comes after the sum has passed 2^31)
+    lens, cu, m = kvq.kvq_plan_append(_plan_only(B, cap, P, pages, table), i32([0] * B), i32(new),
+                                      190, users)
+    assert kvq.kvq_device_error_flags() == kvq.KVQ_DEVERR_CAPACITY | kvq.KVQ_DEVERR_NO_PAGE
+    assert lens.tolist() == [150, 0, 40] + [0] * (B - 3) and cu.tolist() == _summed(new)
+    assert table[0, :5].tolist() == [1, 2, 4, 5, 7] and table[2, :2].tolist() == [8, 10]
+    assert int((table >= 0).sum()) == 7 and int((users != 0).sum()) == (pages + 2) // 3 + 7
+    got = [e for e in m.tolist() if e[3]]
+    assert len(got) == 10 + 3 and sum(e[3] for e in got) == 190
+    assert got[-1] == [10, 0, 182, 8]
