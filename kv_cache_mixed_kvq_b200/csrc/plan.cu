@@ -321,9 +321,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
   const size_t smem = sizeof(int) * 3 * static_cast<size_t>(a.batch);
   if (smem > 48 * 1024) {
-    // (once per call: it costs less than keeping track of the devices)
-    const cudaError_t e = cudaFuncSetAttribute(
-        plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // The limit is one of the function and the device, whatever thread sets it:
+    // always that of the largest batch, so that no call lowers another's
+    // between its set and its launch.  (Once per call: it costs less than
+    // keeping track of the devices.)
+    const cudaError_t e =
+        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sizeof(int)) * 3 * kPlanRows);
     if (e != cudaSuccess) return e;
   }
   const int parts = a.num_pages > kSmallPool ? kPlanCluster : 1;

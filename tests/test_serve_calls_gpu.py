@@ -1,6 +1,9 @@
 """GPU tests of how the serving step is called: on which stream a call's
 memory lives, from several host threads, with padded batches, with values that
 are not finite, and with waits that run out."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -227,3 +230,36 @@ def test_plan_of_more_pages_than_32_bits_count(pages):
     got = [e for e in m.tolist() if e[3]]
     assert len(got) == 10 + 3 and sum(e[3] for e in got) == 190
     assert got[-1] == [10, 0, 182, 8]
+
+
+# ------------------------------------------------------- several host threads
+def test_threads_plan_batches_of_different_sizes():
+    """The kernel's shared-memory limit is the function's, not a thread's."""
+    lib, ready, statuses = kvq.library(), threading.Barrier(6), []
+
+    def prepare(B):
+        cache, old, new = _plan_only(B, 64), i32([0] * B), i32([1] * B)
+        lens, cu = torch.empty_like(old), i32([0] * (B + 1))
+        m = torch.empty(B, 4, dtype=torch.int32, device="cuda")
+        s = torch.cuda.Stream()
+        args = (ctypes.byref(cache.desc()), old.data_ptr(), new.data_ptr(), B, None,
+                lens.data_ptr(), cu.data_ptr(), m.data_ptr(), B, s.cuda_stream)
+        return args, (cache, old, new, lens, cu, m, s)
+
+    jobs = [prepare(B) for B in (8192, 4500, 8000, 5000, 7000, 4200)]
+    torch.cuda.synchronize()
+
+    def work(args):
+        ready.wait()
+        statuses.append({lib.kvq_plan_append(*args) for _ in range(3000)})
+
+    threads = [threading.Thread(target=work, args=(args,)) for args, _ in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert statuses == [{kvq.KVQ_OK}] * 6
+    for _, (_, _, new, lens, cu, _, _) in jobs:
+        assert torch.equal(lens, new) and cu[-1].item() == new.numel()
+    assert kvq.kvq_device_error_flags() == 0
