@@ -28,8 +28,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
   if (a.stream_q > 0) {
     // balanced schedule: the CTAs that covered this row's unit, from the same
     // prefix sums as the decode kernel (built from the lengths alone, before
-    // the wait for the decode grid); a unit one CTA covered whole was written
-    // by it directly
+    // the wait for the decode grid: see below); a unit one CTA covered whole
+    // was written by it directly
     __shared__ int s_off[kStreamRows + 1];
     __shared__ int s_w[4];
     const int units = a.kv_heads * a.head_groups;  // per row
@@ -48,8 +48,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
       if (ns == 1) return;
     }
   } else {
-    // (the lengths are read before the wait: no kernel of this library
-    // writes them)
+    // (the lengths are read before the wait for the decode grid: its CTAs let
+    // this one start after their own wait, when whatever wrote the lengths,
+    // the planner for one, has completed)
     const int len = max(0, min(a.seq_lens[b], lim));
     ns = (len + a.split_tokens - 1) / a.split_tokens;
     pdl_wait();

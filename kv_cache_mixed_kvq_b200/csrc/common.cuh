@@ -80,9 +80,8 @@ __device__ __forceinline__ void flag_error(uint32_t* err, uint32_t bits) {
 // off[r] = units * sum_{r' < r} ceil(len_r' / T) for r = 0 .. kStreamRows,
 // with each length clamped to [0, lim] (rows past `batch` count nothing);
 // lens (when not NULL): the raw lengths, kStreamRows entries (0 past
-// `batch`).  Reads only the lengths, so it may run before the wait for the
-// previous grid.  Called by all 128 threads of the CTA; wsum: 4 ints of
-// shared scratch.  Ends with a CTA barrier.
+// `batch`).  Reads only the lengths.  Called by all 128 threads of the CTA;
+// wsum: 4 ints of shared scratch.  Ends with a CTA barrier.
 __device__ __forceinline__ void stream_row_offsets(const int32_t* seq_lens, int batch, int lim,
                                                    int units, int T, int* off, int* lens,
                                                    int* wsum) {

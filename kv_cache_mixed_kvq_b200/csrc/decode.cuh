@@ -1121,9 +1121,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
   const int lim = min(a.max_seq_len, a.capacity);
   const bool stream = a.stream_q > 0;
 
-  // balanced schedule: the rows' lengths and the prefix sums of their stages,
-  // built before the wait for the previous grid (no kernel of this library
-  // writes the lengths; the ring is free scratch until the first span)
+  pdl_wait();
+  pdl_trigger();
+  // balanced schedule: the rows' lengths and the prefix sums of their stages
+  // (after the wait: the previous grid may be the planner, which writes the
+  // lengths; the ring is free scratch until the first span)
   int* lens = reinterpret_cast<int*>(smem + C::SMEM_BYTES - 4 * (2 * kStreamRows + 1));
   int* off = lens + kStreamRows;
   const int U = a.kv_heads * a.head_groups;
@@ -1137,8 +1139,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     // the row holding stage p (rows with no stages are skipped)
     while (rb < a.batch - 1 && off[rb + 1] <= p) ++rb;
   }
-  pdl_wait();
-  pdl_trigger();
   if (stream && blockIdx.x == 0)
     for (int r = threadIdx.x; r < a.batch; r += C::kThreads)
       if (lens[r] < 0 || lens[r] > lim) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);

@@ -263,3 +263,31 @@ def test_threads_plan_batches_of_different_sizes():
     for _, (_, _, new, lens, cu, _, _) in jobs:
         assert torch.equal(lens, new) and cu[-1].item() == new.numel()
     assert kvq.kvq_device_error_flags() == 0
+
+
+# -------------------------------------------------------- launches in a chain
+@pytest.mark.parametrize("schedule", ["splits", "balanced"])
+def test_attention_right_after_the_plan_that_writes_its_lengths(schedule, monkeypatch):
+    """The decode kernel may start while the planner still runs: it reads the
+    lengths only after it, with either division of the work."""
+    if schedule == "balanced":
+        monkeypatch.setenv("KVQ_DECODE_SCHEDULE", "balanced")
+    B, P, cap, pages = 64, 32, 1024, 1 << 20  # (many pages: the planner takes its time)
+    planned = _plan_only(B, cap, P, pages, torch.full((B, cap // P), -1, dtype=torch.int32,
+                                                      device="cuda"))
+    users = torch.ones(pages, dtype=torch.int32, device="cuda")
+    users[-30000:] = 0
+    cache, _ = make_cache(B, 1, 64, cap, 4, 2, 64)
+    fill(cache, None, [cap] * B, 1)
+    q, none = tokens(B, 4, 64, "bf16", 3), i32([0] * B)
+    steps = [i32([1 + (37 * b + 211 * i) % cap for b in range(B)]) for i in range(12)]
+    want = [kvq.kvq_decode_attention(cache, q, new, cap) for new in steps]
+    torch.cuda.synchronize()
+    got = []
+    for new in steps:
+        lens = kvq.kvq_plan_append(planned, none, new, B * cap, users)[0]
+        got.append(kvq.kvq_decode_attention(cache, q, lens, cap))
+    torch.cuda.synchronize()
+    assert kvq.kvq_device_error_flags() == 0
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
