@@ -511,8 +511,7 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  *                 cu_tokens[B] on are left as they were in out.
  *   seq_lens    : device int32[B]: cached positions of each row, its new
  *                 tokens among them.
- *   max_q_len   : host upper bound of every row's n_b; when it is 1 and
- *                 num_tokens = B, every row has to have its one token.
+ *   max_q_len   : host upper bound of every row's n_b.
  *   max_seq_len : host upper bound of seq_lens.
  *   sm_scale    : softmax scale; <= 0 selects 1/sqrt(D).
  *   out         : device, [num_tokens][Hq][D] packed, out_dtype, 16-byte aligned.
@@ -528,8 +527,8 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  * within 2^30 (KVQ_ERR_UNSUPPORTED above).
  *
  * Kernel launches: one, and a second one that joins partial results when rows
- * are long enough to be divided; rows of one 16-bit token each go to
- * kvq_decode_attention().  Arithmetic: products of binary16 operands on the
+ * are long enough to be divided; 16-bit queries of max_q_len = 1 and
+ * num_tokens = B go to the decode kernel.  Arithmetic: products of binary16 operands on the
  * tensor cores with binary32 sums; a key, value or query is rounded once to
  * binary16 when the queries are bf16, and held in two binary16 halves (2^-22)
  * where that would be coarser than the query's type (keys and values for f16,

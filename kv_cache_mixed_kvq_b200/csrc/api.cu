@@ -439,9 +439,12 @@ int32_t kvq_decode_split_tokens(const kvq_cache_desc* cache, int32_t num_q_heads
 }  // extern "C"
 
 namespace {
-// Decode attention, with the step's append fused in when k_new != NULL.
+// Decode attention, with the step's append fused in when k_new != NULL, or of
+// the batch rows' tokens at cu (a plain decode in the split schedule by the
+// register-fragment kernel, which alone looks rows up).
 int decode_impl(const kvq_cache_desc* cache, const void* k_new, const void* v_new,
-                int32_t in_dtype, int32_t n_new, const void* q, int32_t q_dtype,
+                int32_t in_dtype, int32_t n_new, const int32_t* cu, int32_t num_tokens,
+                const void* q, int32_t q_dtype,
                 int32_t num_q_heads, const int32_t* seq_lens, int32_t max_seq_len,
                 float sm_scale, void* out, int32_t out_dtype, void* workspace,
                 size_t workspace_bytes, kvq_stream_t stream) {
@@ -464,11 +467,12 @@ int decode_impl(const kvq_cache_desc* cache, const void* k_new, const void* v_ne
   bool balanced = false;  // the balanced (stream-K) schedule runs
   if (p.num_splits > 0) {
     DecodeKernel k;
-    if (!select_decode_kernel(cache, p.heads_per_cta, q_dtype, k_new != nullptr, &k))
+    if (!select_decode_kernel(cache, p.heads_per_cta, q_dtype, k_new != nullptr || cu != nullptr,
+                              &k))
       return KVQ_ERR_UNSUPPORTED;
     // the balanced schedule serves the kernel it was planned for (both the
     // plain and the fused decode, so that they take the same splits)
-    balanced = p.stream_q > 0 && k.stage_tokens == p.stage_tokens;
+    balanced = p.stream_q > 0 && k.stage_tokens == p.stage_tokens && cu == nullptr;
     if (prepare_kernel(k) != cudaSuccess) return KVQ_ERR_CUDA;
     kvq::DecodeArgs a;
     a.k_codes = cache->k_codes;
@@ -478,6 +482,8 @@ int decode_impl(const kvq_cache_desc* cache, const void* k_new, const void* v_ne
     a.q = q;
     a.q_dtype = q_dtype;
     a.seq_lens = seq_lens;
+    a.cu = cu;
+    a.num_tokens = num_tokens;
     a.batch = cache->batch;
     a.kv_heads = cache->kv_heads;
     a.q_heads = num_q_heads;
@@ -523,6 +529,8 @@ int decode_impl(const kvq_cache_desc* cache, const void* k_new, const void* v_ne
   ca.ws_o = ws_o;
   ca.ws_lse = ws_lse;
   ca.seq_lens = seq_lens;
+  ca.cu = cu;
+  ca.num_tokens = num_tokens;
   ca.out = out;
   ca.out_dtype = out_dtype;
   ca.batch = cache->batch;
@@ -543,13 +551,23 @@ int decode_impl(const kvq_cache_desc* cache, const void* k_new, const void* v_ne
 }
 }  // namespace
 
+int kvq::decode_single_tokens(const kvq_cache_desc* cache, const void* q, int32_t q_dtype,
+                              int32_t num_q_heads, int32_t num_tokens, const int32_t* cu_tokens,
+                              const int32_t* seq_lens, int32_t max_seq_len, float sm_scale,
+                              void* out, int32_t out_dtype, void* workspace,
+                              size_t workspace_bytes, kvq_stream_t stream) {
+  return decode_impl(cache, nullptr, nullptr, 0, 0, cu_tokens, num_tokens, q, q_dtype, num_q_heads,
+                     seq_lens, max_seq_len, sm_scale, out, out_dtype, workspace, workspace_bytes,
+                     stream);
+}
+
 extern "C" {
 
 int kvq_decode_attention(const kvq_cache_desc* cache, const void* q, int32_t q_dtype,
                          int32_t num_q_heads, const int32_t* seq_lens, int32_t max_seq_len,
                          float sm_scale, void* out, int32_t out_dtype, void* workspace,
                          size_t workspace_bytes, kvq_stream_t stream) {
-  return decode_impl(cache, nullptr, nullptr, 0, 0, q, q_dtype, num_q_heads, seq_lens,
+  return decode_impl(cache, nullptr, nullptr, 0, 0, nullptr, 0, q, q_dtype, num_q_heads, seq_lens,
                      max_seq_len, sm_scale, out, out_dtype, workspace, workspace_bytes, stream);
 }
 
@@ -563,7 +581,7 @@ int kvq_append_decode_attention(const kvq_cache_desc* cache, const void* k_new,
                                   !aligned(k_new, 16) || !aligned(v_new, 16))))
     return KVQ_ERR_INVALID_ARG;
   return decode_impl(cache, n_new > 0 ? k_new : nullptr, n_new > 0 ? v_new : nullptr, in_dtype,
-                     n_new, q, q_dtype, num_q_heads, seq_lens, max_seq_len, sm_scale, out,
+                     n_new, nullptr, 0, q, q_dtype, num_q_heads, seq_lens, max_seq_len, sm_scale, out,
                      out_dtype, workspace, workspace_bytes, stream);
 }
 

@@ -136,10 +136,10 @@ int chunk_plan(const kvq_cache_desc* c, int Hq, int num_tokens, int max_q_len, i
   return KVQ_OK;
 }
 
-// One token in every batch row, of a 16-bit type: the decode kernel's case
-// (max_q_len and num_tokens leave nothing else).
-bool is_decode(const kvq_cache_desc* c, int num_tokens, int max_q_len) {
-  return max_q_len == 1 && num_tokens == c->batch;
+// As many tokens as batch rows, one a row at most: a decode step, some of its
+// rows idle perhaps, which is the decode kernel's case for 16-bit types.
+bool is_decode(const kvq_cache_desc* c, int num_tokens, int max_q_len, int max_seq_len) {
+  return max_q_len == 1 && num_tokens == c->batch && max_seq_len > 0;
 }
 
 // Workspace of a call, whatever its element types (arguments checked).
@@ -151,7 +151,7 @@ size_t chunk_workspace(const kvq_cache_desc* c, int Hq, int num_tokens, int max_
     if (chunk_plan(c, Hq, num_tokens, max_q_len, max_seq_len, pieces, &p) != KVQ_OK) return 0;
     need = std::max(need, p.bytes);
   }
-  if (is_decode(c, num_tokens, max_q_len))
+  if (is_decode(c, num_tokens, max_q_len, max_seq_len))
     need = std::max(need, kvq_decode_workspace_bytes(c, Hq, max_seq_len));
   return need;
 }
@@ -238,10 +238,11 @@ int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_st
       !aligned(cu_tokens, 4) || !aligned(seq_lens, 4) ||
       !valid_stride(q_stride, num_q_heads, cache->head_dim, q_dtype))
     return KVQ_ERR_INVALID_ARG;
-  if (is_decode(cache, num_tokens, max_q_len) && q_dtype != KVQ_F32 &&
+  if (is_decode(cache, num_tokens, max_q_len, max_seq_len) && q_dtype != KVQ_F32 &&
       q_stride == static_cast<int64_t>(num_q_heads) * cache->head_dim)
-    return kvq_decode_attention(cache, q, q_dtype, num_q_heads, seq_lens, max_seq_len, sm_scale,
-                                out, out_dtype, workspace, workspace_bytes, stream);
+    return decode_single_tokens(cache, q, q_dtype, num_q_heads, num_tokens, cu_tokens, seq_lens,
+                                max_seq_len, sm_scale, out, out_dtype, workspace, workspace_bytes,
+                                stream);
   const int pieces = pieces_of(cache, q_dtype);
   ChunkPlan p;
   st = chunk_plan(cache, num_q_heads, num_tokens, max_q_len, max_seq_len, pieces, &p);

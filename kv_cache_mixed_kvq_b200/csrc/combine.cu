@@ -56,6 +56,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
     pdl_wait();
     pdl_trigger();
   }
+  int out_row = row;
+  if (__builtin_expect(a.cu != nullptr, 0)) {
+    const int token = single_token_row(a.cu, a.num_tokens, b);
+    if (token < 0) return;
+    out_row += (token - b) * a.q_heads;
+  }
   const size_t base = static_cast<size_t>(row) * a.num_splits;
 
   // Warp w merges splits w, w+4, w+8, ... with its own running maximum M;
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
     dd = fmaf(f, s_den[w], dd);
   }
   const float val = ns > 0 ? num / dd : 0.0f;
-  const size_t out = static_cast<size_t>(row) * D + d;
+  const size_t out = static_cast<size_t>(out_row) * D + d;
   if (a.out_dtype == KVQ_F32)
     reinterpret_cast<float*>(a.out)[out] = val;
   else if (a.out_dtype == KVQ_BF16)

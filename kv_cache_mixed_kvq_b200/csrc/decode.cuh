@@ -256,13 +256,21 @@ struct Span {
   bool direct;
 };
 
+// Row of q and out of batch row b (whose offsets were checked).  The fused
+// append and the balanced schedule have no offsets.
+template <bool FUSED>
+__device__ __forceinline__ size_t token_row(const DecodeArgs& a, int b) {
+  if (!FUSED && __builtin_expect(a.cu != nullptr, 0)) b = __ldg(a.cu + b);
+  return static_cast<size_t>(b);
+}
+
 // Bulk copy of span s's query rows (heads head0 .. head0 + nh - 1 of row
-// b, [head][D] in the query type) into a query buffer; thread 0 only.  The
+// `row` of q, [head][D] in the query type) into a query buffer; thread 0 only.  The
 // rows are contiguous, start on a multiple of 128 bytes from the query base
 // (16-byte aligned, as the API requires) and are whole 16-byte units.
 template <class C>
-__device__ __forceinline__ void issue_q_rows(const DecodeArgs& a, const Span& s, uint8_t* dst,
-                                             uint64_t* bar) {
+__device__ __forceinline__ void issue_q_rows(const DecodeArgs& a, const Span& s, size_t row,
+                                             uint8_t* dst, uint64_t* bar) {
   const int head0 = s.hk * a.gq + s.hg * a.heads_per_cta;
   const int nh = min(a.heads_per_cta, a.gq - s.hg * a.heads_per_cta);
   const int es = a.q_dtype == KVQ_F32 ? 4 : 2;
@@ -270,7 +278,7 @@ __device__ __forceinline__ void issue_q_rows(const DecodeArgs& a, const Span& s,
   mbar_arrive_expect_tx(bar, bytes);
   bulk_copy_g2s(dst,
                 static_cast<const uint8_t*>(a.q) +
-                    (static_cast<size_t>(s.b) * a.q_heads + head0) * C::D * es,
+                    (row * a.q_heads + head0) * C::D * es,
                 bytes, bar);
 }
 
@@ -388,7 +396,7 @@ __device__ __forceinline__ bool decode_span(const DecodeArgs& a, uint8_t* smem, 
     const int qs = ctl[0];
     ctl[1] = 0;
     if (peek(s)) {
-      issue_q_rows<C>(a, s, qbuf + ((qs + 1) & 1) * C::QBUF_BYTES, &qfull[(qs + 1) & 1]);
+      issue_q_rows<C>(a, s, s.b, qbuf + ((qs + 1) & 1) * C::QBUF_BYTES, &qfull[(qs + 1) & 1]);
       ctl[1] = 1;
     }
   }
@@ -507,7 +515,7 @@ __device__ __forceinline__ bool decode_span(const DecodeArgs& a, uint8_t* smem, 
       float* qs = reinterpret_cast<float*>(wbuf);  // [head][D]
       for (int i = threadIdx.x; i < nh * D; i += C::kThreads)
         qs[i] = load_elem(a.q, a.q_dtype,
-                          (static_cast<size_t>(b) * a.q_heads + head0 + i / D) * D + i % D);
+                          (token_row<FUSED>(a, b) * a.q_heads + head0 + i / D) * D + i % D);
       __syncthreads();
 #pragma unroll 1
       for (int h = 1; h < D; h *= 2) {
@@ -1066,6 +1074,7 @@ __device__ __forceinline__ bool decode_span(const DecodeArgs& a, uint8_t* smem, 
   }
   if (threadIdx.x == 0) ++ctl[0];  // every thread read it in the prologue
   __syncthreads();
+  const size_t row = token_row<FUSED>(a, b);
   for (int idx = threadIdx.x; idx < nh * D; idx += C::kThreads) {
     const int head = idx / D, d = idx % D;
     float num = 0.0f;
@@ -1073,11 +1082,10 @@ __device__ __forceinline__ bool decode_span(const DecodeArgs& a, uint8_t* smem, 
     for (int w = 0; w < C::kWarps; ++w)
       num = fmaf(wt[head * C::kWarps + w], ob[(w * C::OB_HEADS + head) * D + d] + zb[(w * 8 + head) * NGV + d / GV], num);
     if (direct) {
-      store_out(a.out, a.out_dtype, (static_cast<size_t>(b) * a.q_heads + head0 + head) * D + d,
-                num * rden[head]);
+      store_out(a.out, a.out_dtype, (row * a.q_heads + head0 + head) * D + d, num * rden[head]);
     } else {
-      const size_t row = (static_cast<size_t>(b) * a.q_heads + head0 + head) * ws_stride + ws_index;
-      a.ws_o[row * D + d] = num * rden[head];
+      const size_t part = (static_cast<size_t>(b) * a.q_heads + head0 + head) * ws_stride + ws_index;
+      a.ws_o[part * D + d] = num * rden[head];
     }
   }
   return aborted;
@@ -1121,16 +1129,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
   const int lim = min(a.max_seq_len, a.capacity);
   const bool stream = a.stream_q > 0;
 
-  pdl_wait();
-  pdl_trigger();
   // balanced schedule: the rows' lengths and the prefix sums of their stages
-  // (after the wait: the previous grid may be the planner, which writes the
-  // lengths; the ring is free scratch until the first span)
+  // (after the wait for the previous grid: it may be the planner, which writes
+  // the lengths; the ring is free scratch until the first span)
   int* lens = reinterpret_cast<int*>(smem + C::SMEM_BYTES - 4 * (2 * kStreamRows + 1));
   int* off = lens + kStreamRows;
   const int U = a.kv_heads * a.head_groups;
   int p = 0, p_end = 0, Q = 1, rb = 0;
   if (stream) {
+    pdl_wait();
     stream_row_offsets(a.seq_lens, a.batch, lim, U, T, off, lens, reinterpret_cast<int*>(smem));
     const int S = off[kStreamRows];  // rows past the batch count no stages
     Q = max(a.stream_q, (S + gridDim.x - 1) / gridDim.x);
@@ -1139,6 +1146,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     // the row holding stage p (rows with no stages are skipped)
     while (rb < a.batch - 1 && off[rb + 1] <= p) ++rb;
   }
+  pdl_wait();
+  pdl_trigger();
   if (stream && blockIdx.x == 0)
     for (int r = threadIdx.x; r < a.batch; r += C::kThreads)
       if (lens[r] < 0 || lens[r] > lim) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);
@@ -1177,7 +1186,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
   // the first span's query rows are requested first (query buffer 0)
   const bool q_bulk = !a.rotate_q;
   auto first_q = [&]() {
-    if (q_bulk && threadIdx.x == 0) issue_q_rows<C>(a, cur, smem + C::QBUF_OFF, &qfull[0]);
+    if (q_bulk && threadIdx.x == 0)
+      issue_q_rows<C>(a, cur, token_row<FUSED>(a, cur.b), smem + C::QBUF_OFF, &qfull[0]);
   };
   if (stream) {
     if (p >= p_end) return;
@@ -1210,6 +1220,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       if (k == 0 && unit == 0 && threadIdx.x == 0) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);
       len = max(0, min(len, lim));
     }
+    if (!FUSED && __builtin_expect(a.cu != nullptr, 0)) {
+      const int row = single_token_row(a.cu, a.num_tokens, cur.b);
+      if (row < 0) {
+        if (row == -2 && k == 0 && unit == 0 && threadIdx.x == 0)
+          flag_error(a.err, KVQ_DEVERR_BAD_POS);
+        return;
+      }
+    }
     int split = k;
     if constexpr (FUSED) {
       const int ns = (len + a.split_tokens - 1) / a.split_tokens;
@@ -1223,7 +1241,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       if (a.direct && len == 0 && split == 0)
         for (int i = threadIdx.x; i < nh * D; i += C::kThreads)
           store_out(a.out, a.out_dtype,
-                    (static_cast<size_t>(cur.b) * a.q_heads + head0 + i / D) * D + i % D, 0.0f);
+                    (token_row<FUSED>(a, cur.b) * a.q_heads + head0 + i / D) * D + i % D, 0.0f);
       return;
     }
     cur.t1 = min(cur.t0 + a.split_tokens, len);

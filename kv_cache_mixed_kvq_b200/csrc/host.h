@@ -26,4 +26,12 @@ void page_args(const kvq_cache_desc* c, const int32_t** table, int* shift, int* 
 // Device address of the error word on the current device; a kvq_status.
 int error_word(uint32_t** out);
 
+// Decode attention of batch rows that bring one token each at most: row b's is
+// row cu_tokens[b] of q and out ([num_tokens][Hq][D]).
+int decode_single_tokens(const kvq_cache_desc* cache, const void* q, int32_t q_dtype,
+                         int32_t num_q_heads, int32_t num_tokens, const int32_t* cu_tokens,
+                         const int32_t* seq_lens, int32_t max_seq_len, float sm_scale, void* out,
+                         int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                         kvq_stream_t stream);
+
 }  // namespace kvq

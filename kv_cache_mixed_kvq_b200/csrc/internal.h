@@ -65,6 +65,11 @@ struct DecodeArgs {
   const void* q;
   int q_dtype;
   const int32_t* seq_lens;
+  // Ragged serving step (NULL: batch row b's query and output are row b of q
+  // and out): they are row cu[b], of num_tokens; a batch row without a token
+  // (cu[b + 1] = cu[b]) is skipped, one whose offsets are unusable flagged.
+  const int32_t* cu;
+  int num_tokens;
   int batch, kv_heads, q_heads, gq, capacity, max_seq_len;
   int heads_per_cta;  // <= 8
   int head_groups;    // ceil(gq / heads_per_cta)
@@ -128,6 +133,8 @@ struct CombineArgs {
   const float* ws_o;
   const float* ws_lse;
   const int32_t* seq_lens;
+  const int32_t* cu;  // as in DecodeArgs
+  int num_tokens;
   void* out;
   int out_dtype;
   int batch, q_heads, head_dim, capacity, max_seq_len, split_tokens, num_splits;

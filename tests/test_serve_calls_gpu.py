@@ -291,3 +291,45 @@ def test_attention_right_after_the_plan_that_writes_its_lengths(schedule, monkey
     assert kvq.kvq_device_error_flags() == 0
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+# ------------------------------------------------- padded and idle single tokens
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("P,rot,Hq", [(0, False, 8), (64, False, 14), (64, True, 8), (0, True, 32)])
+@pytest.mark.parametrize("long", [False, True])
+def test_single_tokens_of_padded_steps(long, P, rot, Hq, dtype):
+    """As many packed tokens as rows, but some rows idle: each token goes with
+    its own row, and the padding behind the last one is left as it was."""
+    lens = [100, 3000, 64, 1, 2111, 0] if long else [100, 130, 64, 1, 33, 0]
+    cache, users = make_cache(6, 2, 128, 4096, 4, 2, 64, 0, rot, P, 3, want=lens)
+    kd, vd, cu_kv = fill(cache, users, lens, 1)
+    q = tokens(6, Hq, 128, dtype, 9)
+    for cu in ([0, 1, 1, 2, 3, 3, 4], [0, 0, 1, 1, 1, 2, 2], [0, 1, 2, 3, 4, 5, 6], [0] * 7):
+        out = torch.full_like(q, 7.0)
+        kvq.kvq_chunk_attention(cache, q, i32(cu), i32(lens), 1, max(lens), out=out)
+        assert kvq.kvq_device_error_flags() == 0
+        n = cu[-1]
+        assert (out[n:] == 7.0).all()
+        if n:
+            want, tol = attention_reference(q[:n], kd, vd, cu_kv, cu, lens, True, 0.0, q.dtype, rot)
+            assert_close(out[:n], want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("long", [False, True])
+def test_single_tokens_with_unusable_offsets(long, dtype):
+    lens = [3000, 40, 9] if long else [200, 40, 9]
+    cache, users = make_cache(3, 2, 128, 4096, 4, 2, 64, 0, False, 64, 3, want=lens)
+    kd, vd, cu_kv = fill(cache, users, lens, 1)
+    q = tokens(3, 8, 128, dtype, 9)
+    want, tol = attention_reference(q, kd, vd, cu_kv, [0, 1, 2, 3], lens, True, 0.0, q.dtype)
+    # the rows that are served, by offsets with a fault in another row
+    for cu, served in (([0, 1, 3, 3], [0]), ([0, 1, 2, 2 ** 31 - 1], [0, 1]), ([0, 1, 1, 0], [0]),
+                       ([2, 3, 4, 4], None), ([-1, 0, 1, 2], None)):
+        out = torch.full_like(q, 7.0)
+        kvq.kvq_chunk_attention(cache, q, i32(cu), i32(lens), 1, max(lens), out=out)
+        assert kvq.kvq_device_error_flags() == kvq.KVQ_DEVERR_BAD_POS, cu
+        if served is not None:
+            n = len(served)
+            assert_close(out[:n], want[:n], tol[:n])
+            assert (out[n:] == 7.0).all()
