@@ -528,11 +528,12 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  *
  * Kernel launches: one, and a second one that joins partial results when rows
  * are long enough to be divided; 16-bit queries of max_q_len = 1 and
- * num_tokens = B go to the decode kernel.  Arithmetic: products of binary16 operands on the
- * tensor cores with binary32 sums; a key, value or query is rounded once to
- * binary16 when the queries are bf16, and held in two binary16 halves (2^-22)
- * where that would be coarser than the query's type (keys and values for f16,
- * all operands for f32).  Softmax in binary32.
+ * num_tokens = B go to the decode kernel.  Arithmetic: products of binary16
+ * operands on the tensor cores with binary32 sums; a key, value or query is
+ * rounded once to binary16 when the queries are bf16, and held in two binary16
+ * halves (2^-22) where that would be coarser than the query's type (keys,
+ * values and the sums H q of a rotated cache for f16, all operands for f32).
+ * Softmax in binary32.
  */
 int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_stride,
                         int32_t q_dtype, int32_t num_q_heads, int32_t num_tokens,

@@ -467,8 +467,13 @@ int decode_impl(const kvq_cache_desc* cache, const void* k_new, const void* v_ne
   bool balanced = false;  // the balanced (stream-K) schedule runs
   if (p.num_splits > 0) {
     DecodeKernel k;
-    if (!select_decode_kernel(cache, p.heads_per_cta, q_dtype, k_new != nullptr || cu != nullptr,
-                              &k))
+    // A ragged step's rotated binary16 queries take the instances that hold a
+    // query in two binary16 halves: H q / D is a sum, not exact in one (2^-11),
+    // and a row's precision is not to depend on what the other rows bring.
+    const bool halves = cu != nullptr && (cache->flags & KVQ_FLAG_ROTATE_KEYS) != 0 &&
+                        q_dtype == KVQ_F16;
+    if (!select_decode_kernel(cache, p.heads_per_cta, halves ? static_cast<int>(KVQ_F32) : q_dtype,
+                              k_new != nullptr || cu != nullptr, &k))
       return KVQ_ERR_UNSUPPORTED;
     // the balanced schedule serves the kernel it was planned for (both the
     // plain and the fused decode, so that they take the same splits)

@@ -333,3 +333,29 @@ def test_single_tokens_with_unusable_offsets(long, dtype):
             n = len(served)
             assert_close(out[:n], want[:n], tol[:n])
             assert (out[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("P", [0, 64])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 4), (32, 4), (20, 4)])
+def test_rotated_f16_single_tokens_keep_their_query(Hq, Hkv, P):
+    """Scores in the hundreds of two positions that nearly tie: a query rounded
+    to one binary16 would move the weights by 0.01 and more.  The same rows by
+    the decode kernel (as many tokens as rows) and by the tile kernel."""
+    B, D = 96, 128
+    lens = [2 + b % 2 for b in range(B)]
+    cache, users = make_cache(B, Hkv, D, 128, 8, 8, 32, 0, True, P, 1, want=lens)
+    kd, vd, cu_kv = fill(cache, users, lens, 1)
+    q = tokens(B, Hq, D, "f16", 9) * 128.0
+    cu = list(range(B + 1))
+    want, tol = attention_reference(q, kd, vd, cu_kv, cu, lens, True, 0.0, torch.float32, True)
+    # The largest weight of a row is held at 1 or more in binary16, whose
+    # smallest step is 2^-24: a weight less than that part of the largest (the
+    # scores differ by hundreds) may vanish, at most 3 of them, each moving the
+    # output by |v| times as much.
+    tol = tol + 3 * 2.0 ** -24 * vd.abs().max().item()
+    out = kvq.kvq_chunk_attention(cache, q, i32(cu), i32(lens), 1, 3, out_dtype=torch.float32)
+    assert_close(out, want, tol)
+    cu[-1] = B - 1  # the last row idle, its token not there
+    out = kvq.kvq_chunk_attention(cache, q[:-1], i32(cu), i32(lens), 1, 3, out_dtype=torch.float32)
+    assert_close(out, want[:-1], tol[:-1])
+    assert kvq.kvq_device_error_flags() == 0
