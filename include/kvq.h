@@ -533,6 +533,8 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  * rounded once to binary16 when the queries are bf16, and held in two binary16
  * halves (2^-22) where that would be coarser than the query's type (keys,
  * values and the sums H q of a rotated cache for f16, all operands for f32).
+ * (In one half, a group whose largest value passes 65504 by the roundings of
+ * its parameters has its scale lowered, by four binary16 steps at most.)
  * Softmax in binary32.
  */
 int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_stride,

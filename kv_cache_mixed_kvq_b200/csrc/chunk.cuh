@@ -316,10 +316,13 @@ __device__ __forceinline__ __half2 code_field(uint32_t w, int e) {
 }
 
 // The stored roundings of a group's scale and zero can push its largest value
-// past binary16's range (65504); its scale then gives up last places, four at
-// most (2^-8 of a range of 131008 at most, where the roundings are 2^-10).
-template <int B, int N>
+// past binary16's range (65504).  Held in one piece, its scale then gives up
+// last places, four at most (2^-8 of a range of 131008 at most, where the
+// roundings are 2^-10); in two, the high one stops at 65504 and the low one
+// has the rest (see value_pair).  Infinite parameters stay as they are.
+template <int KP, int B, int N>
 __device__ __forceinline__ void fit_range(uint32_t (&scale2)[N], const uint32_t (&zero2)[N]) {
+  if constexpr (KP == 2) return;
   const __half2 top = __float2half2_rn(static_cast<float>((1 << B) - 1));
   auto largest = [&](int i) {
     return __hfma2(top, *reinterpret_cast<const __half2*>(&scale2[i]),
@@ -337,7 +340,11 @@ __device__ __forceinline__ void fit_range(uint32_t (&scale2)[N], const uint32_t 
         const __half2 t = largest(i);
         const uint32_t w = *reinterpret_cast<const uint32_t*>(&t);
         // the next binary16 scale towards zero
-        scale2[i] -= ((w & 0xffffu) == 0x7c00u ? 1u : 0u) + ((w >> 16) == 0x7c00u ? 0x10000u : 0u);
+        auto over = [&](int s) {
+          return ((w >> s) & 0xffffu) == 0x7c00u && ((scale2[i] >> s) & 0xffffu) != 0x7c00u &&
+                 ((zero2[i] >> s) & 0xffffu) != 0x7c00u;
+        };
+        scale2[i] -= (over(0) ? 1u : 0u) + (over(16) ? 0x10000u : 0u);
       }
     }
   }
@@ -354,7 +361,8 @@ __device__ __forceinline__ void value_pair(__half2 code, uint32_t scale2, uint32
   } else {
     const float2 c = __half22float2(code), s = unpack_half2(scale2), z = unpack_half2(zero2);
     const float x = fmaf(c.x, s.x, z.x), y = fmaf(c.y, s.y, z.y);
-    hi = f2_to_h2(x, y);
+    // (65504 at most, see fit_range; infinities and NaN go on in lo)
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
     const float2 h = unpack_half2(hi);
     lo = f2_to_h2(x - h.x, y - h.y);
   }
@@ -409,7 +417,7 @@ __device__ __forceinline__ void unpack_keys(const uint8_t* codes, const uint32_t
     }
     const uint32_t par = live ? params[pos * groups + (32 * span >> gshift)] : 0u;
     uint32_t scale2[1] = {__byte_perm(par, 0, 0x1010)}, zero2[1] = {__byte_perm(par, 0, 0x3232)};
-    fit_range<B>(scale2, zero2);
+    fit_range<C::KP, B>(scale2, zero2);
     uint8_t* half = dst + (span >> 1) * (C::NT * 128);  // 64 elements a swizzled row
     const int x0 = ((span & 1) << 6) ^ rx;
 #pragma unroll
@@ -464,7 +472,7 @@ __device__ __forceinline__ void unpack_values(const uint8_t* codes, const uint32
         scale2[x] = __byte_perm(p0, p1, 0x5410);
         zero2[x] = __byte_perm(p0, p1, 0x7632);
       }
-      fit_range<B>(scale2, zero2);
+      fit_range<C::KP, B>(scale2, zero2);
     }
     uint8_t* dst = col + span * (4 * 8 * 128);
 #pragma unroll

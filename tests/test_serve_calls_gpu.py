@@ -359,3 +359,40 @@ def test_rotated_f16_single_tokens_keep_their_query(Hq, Hkv, P):
     out = kvq.kvq_chunk_attention(cache, q[:-1], i32(cu), i32(lens), 1, 3, out_dtype=torch.float32)
     assert_close(out, want[:-1], tol[:-1])
     assert kvq.kvq_device_error_flags() == 0
+
+
+# --------------------------------------------------- the ends of binary16's range
+@pytest.mark.parametrize("D,bits", [(128, (4, 2)), (64, (2, 8)), (128, (8, 4))])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_largest_values_in_two_halves(dtype, D, bits):
+    """Groups whose stored scale and zero pass 65504 by their roundings are held
+    to 2^-22 like all others where keys and values have two binary16 halves."""
+    cache, _ = make_cache(1, 1, D, 128, *bits, 64)
+    g = torch.Generator().manual_seed(5)
+    x = (torch.rand(100, 1, D, generator=g) * 2 - 1) * 65504.0
+    x[:, :, 0::64], x[:, :, 1::64] = 65504.0, -65504.0 + 16.0 * torch.arange(100).view(100, 1, 1)
+    x = x.cuda()
+    _, _, slots = kvq.kvq_plan_append(cache, i32([0]), i32([100]), 100)
+    kvq.kvq_quantize_append_ragged(cache, x, x, slots)
+    kd, vd = kvq.kvq_dequantize_ragged(cache, slots, 100, torch.float32)
+    assert max(kd.max().item(), vd.max().item()) > 65504.0
+    q = tokens(50, 2, D, dtype, 4)
+    out = kvq.kvq_chunk_attention(cache, q, i32([0, 50]), i32([100]), 50, 100, sm_scale=1e-6,
+                                  out_dtype=torch.float32)
+    want, tol = attention_reference(q, kd, vd, [0, 100], [0, 50], [100], True, 1e-6, torch.float32)
+    assert_close(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("which", ["scale", "zero"])
+def test_visible_value_that_is_infinite(which, dtype):
+    """Infinite parameters are not brought back into range."""
+    cache, _ = make_cache(1, 1, 128, 256, 4, 4, 64)
+    L, t = 200, 130
+    kd, vd, cu_kv = fill(cache, None, [L], 1)
+    cache.v_params.view(torch.float16).view(256, 2, 2)[t, 1, int(which == "zero")] = INF
+    q = tokens(20, 4, 128, dtype, 9)
+    want, tol = attention_reference(q, kd, vd, cu_kv, [0, 20], [L], False, 0.0, q.dtype)
+    out = kvq.kvq_chunk_attention(cache, q, i32([0, 20]), i32([L]), 20, L, causal=False)
+    assert_close(out[..., :64], want[..., :64], tol[..., :64])
+    assert not torch.isfinite(out[..., 64:]).any()
