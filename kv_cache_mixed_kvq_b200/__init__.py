@@ -237,11 +237,18 @@ class KVCache:
         return {k: v for k, v in self.__dict__.items() if k != "_desc"}
 
     def desc(self) -> KvqCacheDesc:
-        """The C descriptor; built again when a field or a buffer's address has
-        changed since the last call."""
+        """The C descriptor: a structure of the caller's own."""
+        return KvqCacheDesc.from_buffer_copy(self._kept_desc())
+
+    def _kept_desc(self) -> KvqCacheDesc:
+        """The descriptor that the calls share; built and checked again when a
+        field, or a buffer's address or layout, has changed since the last one."""
         bt = self.block_table
         at = (self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_params.data_ptr(),
-              self.v_params.data_ptr(), bt.data_ptr() if bt is not None else None)
+              self.v_params.data_ptr(), self.k_codes.is_contiguous(),
+              self.v_codes.is_contiguous(), self.k_params.is_contiguous(),
+              self.v_params.is_contiguous(),
+              (bt.data_ptr(), bt.is_contiguous()) if bt is not None else None)
         kept = self.__dict__.get("_desc")
         if kept is None or kept[0] != at:
             kept = (at, self._build_desc())
@@ -264,7 +271,7 @@ class KVCache:
 
 
 def kvq_validate_cache(cache: KVCache) -> int:
-    d = cache.desc()
+    d = cache._kept_desc()
     return int(library().kvq_validate_cache(ctypes.byref(d)))
 
 
@@ -275,7 +282,7 @@ def kvq_quantize_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: t
         raise ValueError("k and v must be [B][Hkv][n_new][D] tensors of one dtype")
     if pos.dtype != torch.int32:
         raise ValueError("pos must be int32")
-    d = cache.desc()
+    d = cache._kept_desc()
     st = library().kvq_quantize_append(ctypes.byref(d), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
                                        _DTYPE[k.dtype], _dev_ptr(pos, "pos"), k.shape[2],
                                        _stream_ptr(stream))
@@ -284,12 +291,12 @@ def kvq_quantize_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: t
 
 
 def kvq_decode_workspace_bytes(cache: KVCache, num_q_heads: int, max_seq_len: int) -> int:
-    d = cache.desc()
+    d = cache._kept_desc()
     return int(library().kvq_decode_workspace_bytes(ctypes.byref(d), num_q_heads, max_seq_len))
 
 
 def kvq_decode_split_tokens(cache: KVCache, num_q_heads: int, max_seq_len: int) -> int:
-    d = cache.desc()
+    d = cache._kept_desc()
     return int(library().kvq_decode_split_tokens(ctypes.byref(d), num_q_heads, max_seq_len))
 
 
@@ -306,7 +313,7 @@ def kvq_decode_attention(cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor
         raise ValueError("seq_lens must be int32")
     if out is None:
         out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
-    d = cache.desc()
+    d = cache._kept_desc()
     lib = library()
     if workspace is None:  # (a given workspace is checked by the library itself)
         need = int(lib.kvq_decode_workspace_bytes(ctypes.byref(d), q.shape[1], max_seq_len))
@@ -339,7 +346,7 @@ def kvq_append_decode_attention(cache: KVCache, k_new: torch.Tensor, v_new: torc
         raise ValueError("seq_lens must be int32")
     if out is None:
         out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
-    d = cache.desc()
+    d = cache._kept_desc()
     lib = library()
     if workspace is None:  # (a given workspace is checked by the library itself)
         need = int(lib.kvq_decode_workspace_bytes(ctypes.byref(d), q.shape[1], max_seq_len))
@@ -435,7 +442,7 @@ def kvq_plan_append(cache: KVCache, old_lens: torch.Tensor, new_lens: torch.Tens
     slot_map, lens, cu = _empty(4 * E + 2 * B + 1, torch.int32, device,
                                 stream).split_with_sizes((4 * E, B, B + 1))
     slot_map = slot_map.view(E, 4)
-    d = cache.desc()
+    d = cache._kept_desc()
     st = lib.kvq_plan_append(ctypes.byref(d), old, new, num_tokens, users, lens.data_ptr(),
                              cu.data_ptr(), slot_map.data_ptr() if E else None, E,
                              _stream_ptr(stream))
@@ -455,7 +462,7 @@ def kvq_quantize_append_ragged(cache: KVCache, k: torch.Tensor, v: torch.Tensor,
     kp, ks = _tokens(k, cache.kv_heads, cache.head_dim, "k", device)
     vp, vs = _tokens(v, cache.kv_heads, cache.head_dim, "v", device)
     sp = _slots(slot_map, device)
-    d = cache.desc()
+    d = cache._kept_desc()
     st = library().kvq_quantize_append_ragged(ctypes.byref(d), kp, ks, vp, vs, _DTYPE[k.dtype],
                                               k.shape[0], sp, slot_map.shape[0],
                                               _stream_ptr(stream))
@@ -486,7 +493,7 @@ def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: in
                 t.device != device:
             raise ValueError(f"{name} must be {list(shape)}, on the cache's device, of one dtype")
     sp = _slots(slot_map, device)
-    d = cache.desc()
+    d = cache._kept_desc()
     st = library().kvq_dequantize_ragged(ctypes.byref(d), sp, slot_map.shape[0],
                                          _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"),
                                          _DTYPE[k_out.dtype], num_tokens, _stream_ptr(stream))
@@ -497,7 +504,7 @@ def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: in
 
 def kvq_chunk_workspace_bytes(cache: KVCache, num_q_heads: int, num_tokens: int, max_q_len: int,
                               max_seq_len: int) -> int:
-    d = cache.desc()
+    d = cache._kept_desc()
     return int(library().kvq_chunk_workspace_bytes(ctypes.byref(d), num_q_heads, num_tokens,
                                                    max_q_len, max_seq_len))
 
@@ -522,7 +529,7 @@ def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor
         out = _empty((T, Hq, D), out_dtype or q.dtype, device, stream)
     elif out.shape != q.shape or out.dtype not in _DTYPE or out.device != device:
         raise ValueError("out must be of q's shape, on the cache's device")
-    d = cache.desc()
+    d = cache._kept_desc()
     lib = library()
     if workspace is None:  # (a given workspace is checked by the library itself)
         need = lib.kvq_chunk_workspace_bytes(ctypes.byref(d), Hq, T, max_q_len, max_seq_len)
