@@ -149,13 +149,12 @@ def _empty(shape, dtype: torch.dtype, device: torch.device,
     return t
 
 
-def _used_on(stream: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+def _used_on(stream: torch.cuda.Stream, *tensors: Optional[torch.Tensor]) -> None:
     """Marks tensors of other streams as used by the call's, so that their
     memory is not given out again before the call is done with it."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _dev_ptr(t: torch.Tensor, name: str) -> int:
@@ -243,12 +242,10 @@ class KVCache:
     def _kept_desc(self) -> KvqCacheDesc:
         """The descriptor that the calls share; built and checked again when a
         field, or a buffer's address or layout, has changed since the last one."""
-        bt = self.block_table
-        at = (self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_params.data_ptr(),
-              self.v_params.data_ptr(), self.k_codes.is_contiguous(),
-              self.v_codes.is_contiguous(), self.k_params.is_contiguous(),
-              self.v_params.is_contiguous(),
-              (bt.data_ptr(), bt.is_contiguous()) if bt is not None else None)
+        k, v, kp, vp, bt = self._buffers()
+        at = (k.data_ptr(), v.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.is_contiguous(),
+              v.is_contiguous(), kp.is_contiguous(), vp.is_contiguous(),
+              bt is not None and (bt.data_ptr(), bt.is_contiguous()))
         kept = self.__dict__.get("_desc")
         if kept is None or kept[0] != at:
             kept = (at, self._build_desc())
@@ -287,7 +284,8 @@ def kvq_quantize_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pos: t
                                        _DTYPE[k.dtype], _dev_ptr(pos, "pos"), k.shape[2],
                                        _stream_ptr(stream))
     _check(st, "kvq_quantize_append")
-    _used_on(stream, k, v, pos, *cache._buffers())
+    if stream is not None:
+        _used_on(stream, k, v, pos, *cache._buffers())
 
 
 def kvq_decode_workspace_bytes(cache: KVCache, num_q_heads: int, max_seq_len: int) -> int:
@@ -326,7 +324,8 @@ def kvq_decode_attention(cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor
                                   float(sm_scale), _dev_ptr(out, "out"), _DTYPE[out.dtype],
                                   ws_ptr, ws_bytes, _stream_ptr(stream))
     _check(st, "kvq_decode_attention")
-    _used_on(stream, q, seq_lens, out, workspace, *cache._buffers())
+    if stream is not None:
+        _used_on(stream, q, seq_lens, out, workspace, *cache._buffers())
     return out
 
 
@@ -360,7 +359,8 @@ def kvq_append_decode_attention(cache: KVCache, k_new: torch.Tensor, v_new: torc
         _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len), float(sm_scale), _dev_ptr(out, "out"),
         _DTYPE[out.dtype], ws_ptr, ws_bytes, _stream_ptr(stream))
     _check(st, "kvq_append_decode_attention")
-    _used_on(stream, k_new, v_new, q, seq_lens, out, workspace, *cache._buffers())
+    if stream is not None:
+        _used_on(stream, k_new, v_new, q, seq_lens, out, workspace, *cache._buffers())
     return out
 
 
@@ -447,7 +447,8 @@ def kvq_plan_append(cache: KVCache, old_lens: torch.Tensor, new_lens: torch.Tens
                              cu.data_ptr(), slot_map.data_ptr() if E else None, E,
                              _stream_ptr(stream))
     _check(st, "kvq_plan_append")
-    _used_on(stream, old_lens, new_lens, page_users, cache.block_table)
+    if stream is not None:
+        _used_on(stream, old_lens, new_lens, page_users, cache.block_table)
     return lens, cu, slot_map
 
 
@@ -467,7 +468,8 @@ def kvq_quantize_append_ragged(cache: KVCache, k: torch.Tensor, v: torch.Tensor,
                                               k.shape[0], sp, slot_map.shape[0],
                                               _stream_ptr(stream))
     _check(st, "kvq_quantize_append_ragged")
-    _used_on(stream, k, v, slot_map, *cache._buffers())
+    if stream is not None:
+        _used_on(stream, k, v, slot_map, *cache._buffers())
 
 
 def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: int,
@@ -498,7 +500,8 @@ def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: in
                                          _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"),
                                          _DTYPE[k_out.dtype], num_tokens, _stream_ptr(stream))
     _check(st, "kvq_dequantize_ragged")
-    _used_on(stream, slot_map, k_out, v_out, *cache._buffers())
+    if stream is not None:
+        _used_on(stream, slot_map, k_out, v_out, *cache._buffers())
     return k_out, v_out
 
 
@@ -542,7 +545,8 @@ def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor
                                  _dev_ptr(out, "out"), _DTYPE[out.dtype], ws_ptr, ws_bytes,
                                  _stream_ptr(stream))
     _check(st, "kvq_chunk_attention")
-    _used_on(stream, q, cu_tokens, seq_lens, out, workspace, *cache._buffers())
+    if stream is not None:
+        _used_on(stream, q, cu_tokens, seq_lens, out, workspace, *cache._buffers())
     return out
 
 
