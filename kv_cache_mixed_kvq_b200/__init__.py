@@ -259,6 +259,8 @@ class KVCache:
     def _build_desc(self) -> KvqCacheDesc:
         flags = (KVQ_FLAG_ROTATE_KEYS if self.rotate_keys else 0) | \
             (KVQ_FLAG_PAGED if self.page_size else 0)
+        if any(t is not None and t.device != self.k_codes.device for t in self._buffers()):
+            raise ValueError("the cache's buffers must be on one device")
         bt = _dev_ptr(self.block_table, "block_table") if self.block_table is not None else None
         return KvqCacheDesc(self.batch, self.kv_heads, self.head_dim, self.capacity,
                             self.bits_k, self.bits_v, self.group, flags, self.group_v, 0,
@@ -538,6 +540,8 @@ def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor
         need = lib.kvq_chunk_workspace_bytes(ctypes.byref(d), Hq, T, max_q_len, max_seq_len)
         if need > 0:
             workspace = _empty(need, torch.uint8, device, stream, kept=False)
+    elif workspace.device != device:
+        raise ValueError("workspace must be on the cache's device")
     ws_ptr = _dev_ptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib.kvq_chunk_attention(ctypes.byref(d), qp, qs, _DTYPE[q.dtype], Hq, T, cu, lens,

@@ -36,3 +36,27 @@ def test_buffers_are_checked_again_when_their_layout_changes(monkeypatch):
         cache.desc()
     cache.v_params.t_()
     cache.desc()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The kernels would read and write its addresses on the cache's device."""
+    cache = _cache(monkeypatch)
+    monkeypatch.setattr(kvq, "_on_current", lambda device: None)
+    monkeypatch.setattr(kvq, "_stream_ptr", lambda stream: None)
+    q, cu, lens = torch.zeros(4, 4, 128), torch.zeros(3, dtype=torch.int32), \
+        torch.zeros(2, dtype=torch.int32)
+
+    def attend(**kw):
+        # (bounds of no token and length: nothing is launched)
+        return kvq.kvq_chunk_attention(cache, kw.get("q", q)[:0], kw.get("cu", cu),
+                                       kw.get("lens", lens), 0, 0, out=kw.get("out", q)[:0],
+                                       workspace=kw.get("workspace", torch.zeros(64)))
+
+    attend()
+    for name, t in (("q", q), ("cu", cu), ("lens", lens), ("out", q),
+                    ("workspace", torch.zeros(64))):
+        with pytest.raises(ValueError):
+            attend(**{name: t.to("meta")})
+    cache.v_codes = cache.v_codes.to("meta")
+    with pytest.raises(ValueError):
+        attend()
