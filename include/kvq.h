@@ -548,9 +548,10 @@ int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_st
  * Failure-detection test knob; not for production use.  The summary page has
  * no counterpart: it exists so that a test can make a bounded device wait run
  * out without faulting or hanging the GPU.  With drop_stage 0 or 1, the next
- * decode-attention launch in this process (only that one) makes stage
+ * decode- or chunk-attention launch in this process (only that one) makes stage
  * `drop_stage` of the first warp's copy pipeline in its first CTA expect 16
- * bytes more than its copies bring, and every bounded wait of that launch
+ * bytes more than its copies bring (chunk attention: that block of the first
+ * CTA's ring one arrival more), and every bounded wait of that launch
  * gives up after wait_limit_ns (1000 .. 1e9 ns) instead of one second.  The
  * wait on that stage then runs out: the kernel flags KVQ_DEVERR_TIMEOUT,
  * waits (bounded) for its copies in flight, and returns; that call's output

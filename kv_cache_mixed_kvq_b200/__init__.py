@@ -555,7 +555,7 @@ def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_tokens: torch.Tensor
 
 
 def kvq_debug_inject_wait_timeout(drop_stage: int, wait_limit_ns: int = 1_000_000) -> None:
-    """Test knob: in the next decode launch, stage drop_stage (0 or 1) of the
+    """Test knob: in the next decode or chunk launch, stage drop_stage (0 or 1) of the
     first warp's copy pipeline expects more bytes than its copies bring, so
     that a bounded wait runs out (see kvq.h); drop_stage < 0 disarms it."""
     _check(library().kvq_debug_inject_wait_timeout(int(drop_stage), int(wait_limit_ns)),

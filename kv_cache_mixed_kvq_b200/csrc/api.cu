@@ -67,7 +67,7 @@ bool get_decode_kernel(int head_dim, int bits_k, int bits_v, int groups_k, int g
 static __device__ uint32_t g_kvq_device_error;
 
 // Armed failure-detection test knob (kvq_debug_inject_wait_timeout): the
-// stage to drop in the next decode launch (-1: none) and its wait limit.
+// stage to drop in the next decode or chunk attention launch (-1: none) and its wait limit.
 static std::atomic<long long> g_fault_stage{-1};
 static std::atomic<long long> g_fault_limit_ns{0};
 
@@ -155,6 +155,13 @@ int error_word(uint32_t** out) {
   }
   *out = ptrs[dev];
   return KVQ_OK;
+}
+
+int take_fault(unsigned long long* wait_limit_ns) {
+  const long long stage = g_fault_stage.exchange(-1);
+  *wait_limit_ns =
+      stage >= 0 ? static_cast<unsigned long long>(g_fault_limit_ns.load()) : 1000000000ull;
+  return stage >= 0 ? static_cast<int>(stage) : -1;
 }
 
 }  // namespace kvq
@@ -508,11 +515,7 @@ int decode_impl(const kvq_cache_desc* cache, const void* k_new, const void* v_ne
     a.v_new = v_new;
     a.in_dtype = in_dtype;
     a.n_new = n_new;
-    // one-shot test knob: only the next launch after arming it carries it
-    const long long fault = g_fault_stage.exchange(-1);
-    a.fault_stage = fault >= 0 ? static_cast<int>(fault) : -1;
-    a.wait_limit_ns = fault >= 0 ? static_cast<unsigned long long>(g_fault_limit_ns.load())
-                                 : 1000000000ull;
+    a.fault_stage = take_fault(&a.wait_limit_ns);
     a.ws_o = ws_o;
     a.ws_lse = ws_lse;
     a.direct = p.direct && !balanced;

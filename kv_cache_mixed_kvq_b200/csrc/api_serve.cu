@@ -283,6 +283,9 @@ int kvq_chunk_attention(const kvq_cache_desc* cache, const void* q, int64_t q_st
   a.ws_o = reinterpret_cast<float*>(ws ? ws + p.o_offset : nullptr);
   st = error_word(&a.err);
   if (st != KVQ_OK) return st;
+  unsigned long long limit;
+  a.fault_stage = take_fault(&limit);
+  a.wait_limit_ns = static_cast<uint32_t>(limit);  // (a second at most)
   return to_status(launch_chunk(a, pieces, p.grid, reinterpret_cast<cudaStream_t>(stream)));
 }
 

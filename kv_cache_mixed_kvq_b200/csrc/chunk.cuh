@@ -132,6 +132,7 @@ struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2];
   uint64_t q_full, m_full, m_free;
+  uint64_t drained;  // the products in flight when a wait ran out
   uint64_t x_full[2][4];  // [slot][quarter of the rows]: the two halves' maxima
   uint64_t d_full[2], d_empty[2];
   uint64_t ring_full[kRing], ring_empty[kRing];
@@ -148,15 +149,16 @@ static_assert(sizeof(Shared) <= kHeader, "header");
 
 struct Waiter {
   int* abort;
-  // Bounded wait of a warp: false if the phase did not complete within a
-  // second, or if another wait of this CTA gave up (the kernel's end flags it).
+  uint32_t limit_ns;
+  // Bounded wait of a warp: false if the phase did not complete within the
+  // limit, or if another wait of this CTA gave up (the kernel's end flags it).
   // The loop is short: it is part of every role's code.
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
       const uint32_t t0 = timer();
       while (!(ok = mbar_try_wait(bar, parity))) {
-        if (timer() - t0 > static_cast<uint32_t>(kWaitLimitNs))
+        if (timer() - t0 > limit_ns)
           *reinterpret_cast<volatile int*>(abort) = 1;
         if (*reinterpret_cast<volatile int*>(abort) != 0) break;
       }
@@ -1348,9 +1350,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     mbar_init(&sh->q_full, 16);
     mbar_init(&sh->m_full, 8);
     mbar_init(&sh->m_free, 16);
+    mbar_init(&sh->drained, 1);
     for (int i = 0; i < 8; ++i) mbar_init(&sh->x_full[i >> 2][i & 3], 2);
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh->ring_full[i], 32);
+      mbar_init(&sh->ring_full[i], blockIdx.x == 0 && i == a.fault_stage ? 33 : 32);
       mbar_init(&sh->ring_empty[i], 2 * C::PARTS);
     }
     sh->abort = 0;
@@ -1368,7 +1371,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh->tmem;
-  const Waiter wait{&sh->abort};
+  const Waiter wait{&sh->abort, a.wait_limit_ns};
 
   if (warp < kWarpUnpack) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -1409,14 +1412,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     tc::fence_after_sync();
     if (sh->abort != 0) {
       if ((threadIdx.x & 31) == 0) flag_error(a.err, KVQ_DEVERR_TIMEOUT);
-      // products in flight end before their memory is given back
-      if ((threadIdx.x & 31) == 0) {
-        mbar_init(&sh->q_full, 1);
-        fence_barrier_init();
-        tc::commit(&sh->q_full);
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&sh->q_full, 0) && global_timer_ns() - t0 < 10000000ull) {
-        }
+      // products in flight end before their memory is given back (a commit
+      // covers those of the thread that makes it: the one that issued them)
+      if (tc::elect_one()) tc::commit(&sh->drained);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&sh->drained, 0) && global_timer_ns() - t0 < 10000000ull) {
       }
       __syncwarp();
     }

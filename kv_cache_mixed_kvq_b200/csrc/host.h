@@ -26,6 +26,10 @@ void page_args(const kvq_cache_desc* c, const int32_t** table, int* shift, int* 
 // Device address of the error word on the current device; a kvq_status.
 int error_word(uint32_t** out);
 
+// One-shot test knob: the stage that the launch being prepared drops (-1:
+// none), and the limit of its bounded waits.
+int take_fault(unsigned long long* wait_limit_ns);
+
 // Decode attention of batch rows that bring one token each at most: row b's is
 // row cu_tokens[b] of q and out ([num_tokens][Hq][D]).
 int decode_single_tokens(const kvq_cache_desc* cache, const void* q, int32_t q_dtype,

@@ -97,6 +97,12 @@ struct ChunkArgs {
   int* ws_head;
   float2* ws_ml;  // [grid][2][part_rows]: (reference exponent, sum)
   float* ws_o;    // [grid][2][part_rows][D]
+  // Failure-detection test knob (kvq_debug_inject_wait_timeout): when
+  // fault_stage is 0 or 1, that block of the first CTA's ring expects one
+  // arrival more than its copies bring, so that the wait on it runs out; every
+  // bounded wait of the launch gives up after wait_limit_ns.
+  int fault_stage;
+  uint32_t wait_limit_ns;
 };
 
 cudaError_t launch_chunk(const ChunkArgs& a, int pieces, int grid, cudaStream_t stream);

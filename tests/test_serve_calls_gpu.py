@@ -3,6 +3,7 @@ memory lives, from several host threads, with padded batches, with values that
 are not finite, and with waits that run out."""
 import ctypes
 import threading
+import time
 
 import pytest
 import torch
@@ -396,3 +397,39 @@ def test_visible_value_that_is_infinite(which, dtype):
     out = kvq.kvq_chunk_attention(cache, q, i32([0, 20]), i32([L]), 20, L, causal=False)
     assert_close(out[..., :64], want[..., :64], tol[..., :64])
     assert not torch.isfinite(out[..., 64:]).any()
+
+
+# ------------------------------------------------------------ failure detection
+@pytest.mark.parametrize("dtype,D,bits", [("bf16", 128, (4, 2)), ("bf16", 128, (8, 8)),
+                                          ("f16", 128, (4, 2)), ("f32", 64, (2, 4))])
+@pytest.mark.parametrize("lens,n_new", [([200, 90], [60, 2]), ([3000, 40], [4, 40]),
+                                        ([2000], [700])])
+@pytest.mark.parametrize("drop_stage", [0, 1])
+def test_chunk_wait_that_runs_out(drop_stage, lens, n_new, dtype, D, bits):
+    """One ring block of the first CTA never fills up: the launch flags it and
+    ends, with products of other tiles or none in flight, and the next call is
+    as ever.  (No fault and no hang: every wait is bounded, here to 1 ms.)"""
+    cache, users = make_cache(len(lens), 2, D, 4096, *bits, 32, 0, False, 64, 3, want=lens)
+    fill(cache, users, lens, 1)
+    cu = [0]
+    for n in n_new:
+        cu.append(cu[-1] + n)
+    q, at, offsets = tokens(cu[-1], 8, D, dtype, 9), i32(lens), i32(cu)
+    bytes_before = [t.clone() for t in (cache.k_codes, cache.v_codes, cache.k_params)]
+
+    def run():
+        out = kvq.kvq_chunk_attention(cache, q, offsets, at, max(n_new), max(lens))
+        torch.cuda.synchronize()
+        return out
+
+    ref = run()
+    assert kvq.kvq_last_device_error() == 0
+    kvq.kvq_debug_inject_wait_timeout(drop_stage, wait_limit_ns=1_000_000)
+    t0 = time.perf_counter()
+    run()
+    elapsed = time.perf_counter() - t0
+    assert kvq.kvq_last_device_error() == kvq.KVQ_DEVERR_TIMEOUT
+    assert elapsed < 0.5
+    for t, before in zip((cache.k_codes, cache.v_codes, cache.k_params), bytes_before):
+        assert torch.equal(t, before)
+    assert torch.equal(run(), ref) and kvq.kvq_last_device_error() == 0
