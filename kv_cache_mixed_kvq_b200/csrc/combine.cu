@@ -24,7 +24,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
   const int lane = threadIdx.x & 31;
   const int b = row / a.q_heads;
   const int lim = min(a.max_seq_len, a.capacity);
-  int ns;  // partial results of this row
+  int ns;         // partial results of this row
+  int token = b;  // row of the output (in units of q_heads)
   if (a.stream_q > 0) {
     // balanced schedule: the CTAs that covered this row's unit, from the same
     // prefix sums as the decode kernel (built from the lengths alone, before
@@ -48,19 +49,16 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
       if (ns == 1) return;
     }
   } else {
-    // (the lengths are read before the wait for the decode grid: its CTAs let
-    // this one start after their own wait, when whatever wrote the lengths,
-    // the planner for one, has completed)
+    // (the lengths and offsets are read before the wait for the decode grid:
+    // its CTAs let this one start after their own wait, when whatever wrote
+    // them, the planner for one, has completed)
+    if (__builtin_expect(a.cu != nullptr, 0)) token = single_token_row(a.cu, a.num_tokens, b);
     const int len = max(0, min(a.seq_lens[b], lim));
     ns = (len + a.split_tokens - 1) / a.split_tokens;
     pdl_wait();
     pdl_trigger();
-  }
-  int out_row = row;
-  if (__builtin_expect(a.cu != nullptr, 0)) {
-    const int token = single_token_row(a.cu, a.num_tokens, b);
+    // (not before: the grid is not to end before the one that it waits for)
     if (token < 0) return;
-    out_row += (token - b) * a.q_heads;
   }
   const size_t base = static_cast<size_t>(row) * a.num_splits;
 
@@ -135,7 +133,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
     dd = fmaf(f, s_den[w], dd);
   }
   const float val = ns > 0 ? num / dd : 0.0f;
-  const size_t out = static_cast<size_t>(out_row) * D + d;
+  const size_t out = static_cast<size_t>(row + (token - b) * a.q_heads) * D + d;
   if (a.out_dtype == KVQ_F32)
     reinterpret_cast<float*>(a.out)[out] = val;
   else if (a.out_dtype == KVQ_BF16)

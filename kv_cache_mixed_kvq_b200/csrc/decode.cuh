@@ -1185,14 +1185,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
   int adv = 0;
   // the first span's query rows are requested first (query buffer 0)
   const bool q_bulk = !a.rotate_q;
-  auto first_q = [&]() {
-    if (q_bulk && threadIdx.x == 0)
-      issue_q_rows<C>(a, cur, token_row<FUSED>(a, cur.b), smem + C::QBUF_OFF, &qfull[0]);
+  auto first_q = [&](int row) {
+    if (q_bulk && threadIdx.x == 0) issue_q_rows<C>(a, cur, row, smem + C::QBUF_OFF, &qfull[0]);
   };
   if (stream) {
     if (p >= p_end) return;
     stream_span(p, rb, cur, adv);
-    first_q();
+    first_q(cur.b);
   } else {
     // Grid (splits, kv heads x head groups, batch rows).  The fused instance
     // is launched as (kv heads x head groups, batch rows, k) instead, split
@@ -1206,6 +1205,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     cur.hg = unit % a.head_groups;
     cur.b = FUSED ? blockIdx.y : blockIdx.z;
     int len = a.seq_lens[cur.b];
+    int row = cur.b;  // of q and out
+    if (!FUSED && __builtin_expect(a.cu != nullptr, 0))
+      row = single_token_row(a.cu, a.num_tokens, row);
     // fused append: positions [len - n_new, len) are written first; a row
     // whose length is out of range appends nothing
     cur.app_pos = -1;
@@ -1220,13 +1222,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       if (k == 0 && unit == 0 && threadIdx.x == 0) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);
       len = max(0, min(len, lim));
     }
-    if (!FUSED && __builtin_expect(a.cu != nullptr, 0)) {
-      const int row = single_token_row(a.cu, a.num_tokens, cur.b);
-      if (row < 0) {
-        if (row == -2 && k == 0 && unit == 0 && threadIdx.x == 0)
-          flag_error(a.err, KVQ_DEVERR_BAD_POS);
-        return;
-      }
+    if (!FUSED && __builtin_expect(row < 0, 0)) {
+      if (row == -2 && k == 0 && unit == 0 && threadIdx.x == 0)
+        flag_error(a.err, KVQ_DEVERR_BAD_POS);
+      return;
     }
     int split = k;
     if constexpr (FUSED) {
@@ -1241,13 +1240,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       if (a.direct && len == 0 && split == 0)
         for (int i = threadIdx.x; i < nh * D; i += C::kThreads)
           store_out(a.out, a.out_dtype,
-                    (token_row<FUSED>(a, cur.b) * a.q_heads + head0 + i / D) * D + i % D, 0.0f);
+                    (static_cast<size_t>(row) * a.q_heads + head0 + i / D) * D + i % D, 0.0f);
       return;
     }
     cur.t1 = min(cur.t0 + a.split_tokens, len);
     cur.ws_index = split;
     cur.direct = a.direct;
-    first_q();
+    first_q(row);
   }
 
   int g0 = 0, pre = 0;  // this warp's copy stream (see decode_span)
