@@ -42,19 +42,43 @@ def _with_headers(src: str) -> set:
     return seen
 
 
+def check_launch_registers(log: str) -> None:
+    """Checks the assembler's report on the chunk attention kernels: their
+    warpgroups' register split counts on what the launch allocates (registers
+    a thread, in eights); with less it would never be granted."""
+    with open(os.path.join(CSRC, "chunk.cuh")) as f:
+        want = int(re.search(r"kRegsLaunch = (\d+)", f.read()).group(1))
+    kernel, seen = None, 0
+    for line in log.splitlines():
+        m = re.search(r"Compiling entry function '(\S+)'", line)
+        if m:
+            kernel = m.group(1) if "chunk_kernel" in m.group(1) else None
+        m = re.search(r"Used (\d+) registers", line)
+        if m and kernel:
+            seen += 1
+            if (int(m.group(1)) + 7) // 8 * 8 != want:
+                raise RuntimeError(f"{kernel} was given {m.group(1)} registers a thread; the split "
+                                   f"among its warpgroups (csrc/chunk.cuh) needs {want}")
+    if not seen:
+        raise RuntimeError("no report on the registers of the chunk attention kernels")
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     newest = max(os.path.getmtime(p) for p in _with_headers(src))
     if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
         return obj
     cmd = [NVCC] + ARCH + FLAGS + ["-c", src, "-o", obj + ".tmp"]
-    if verbose:
+    splits_registers = os.path.basename(src) == "chunk.cu"
+    if verbose or splits_registers:
         cmd += ["-Xptxas", "-v"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
     if verbose and r.stderr:
         sys.stderr.write(r.stderr)
+    if splits_registers:
+        check_launch_registers(r.stderr)
     os.replace(obj + ".tmp", obj)
     return obj
 

@@ -54,8 +54,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const ChunkArgs a, int gri
   }
 }
 
-// Opts the kernel in to its shared memory, once per device; refuses a build
-// whose register count is not the one that the kernel's split counts on.
+// Opts the kernel in to its shared memory, once per device; refuses a library
+// whose launches would not allocate the registers that the kernel's split counts
+// on (the build checks the same, with a message).
 cudaError_t prepare(const void* fn) {
   static std::mutex mu;
   static std::set<std::pair<int, const void*>> done;
@@ -66,7 +67,8 @@ cudaError_t prepare(const void* fn) {
   if (done.count({dev, fn})) return cudaSuccess;
   cudaFuncAttributes attr;
   e = cudaFuncGetAttributes(&attr, fn);
-  if (e == cudaSuccess && attr.numRegs != chunk::kRegsLaunch) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && (attr.numRegs + 7) / 8 * 8 != chunk::kRegsLaunch)
+    e = cudaErrorInvalidConfiguration;
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, chunk::kSmemMax);
   if (e == cudaSuccess) done.insert({dev, fn});

@@ -83,7 +83,7 @@ constexpr int kWarpUnpack = 16, kWarpMma = 24, kWarpList = 25, kWarpCopy = 26;
 constexpr int kCopiers = 2;       // warps that copy, block by block in turn
 // Registers a thread at launch, and of each warpgroup after the split: 512 x 80
 // + 256 x 64 + 128 x 56 <= 896 x 72.  (Seven warps share an SM quarter's 16384
-// registers, hence 72.)
+// registers, hence 72: what 65 to 72 allocate, in eights.)
 constexpr int kRegsLaunch = 72, kRegsSoftmax = 80, kRegsUnpack = 64, kRegsIssue = 56;
 static_assert(512 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kThreads * kRegsLaunch,
               "more registers than the launch has would never be granted");

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import kv_cache_mixed_kvq_b200 as kvq
+from kv_cache_mixed_kvq_b200 import build
 
 
 def _cache(monkeypatch):
@@ -60,3 +61,23 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     cache.v_codes = cache.v_codes.to("meta")
     with pytest.raises(ValueError):
         attend()
+
+
+def _report(kernel, registers):
+    return (f"ptxas info    : Compiling entry function '{kernel}' for 'sm_100a'\n"
+            f"ptxas info    : Function properties for {kernel}\n"
+            "    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads\n"
+            f"ptxas info    : Used {registers} registers, used 1 barriers\n")
+
+
+def test_build_checks_the_registers_of_the_split_kernels():
+    """A compiler that gives the kernel fewer registers is noticed by the build;
+    one that stays within the same allocation is no reason to refuse."""
+    good = "_ZN3kvq5chunk12chunk_kernelINS0_3CfgE"
+    for n in (65, 70, 72):
+        build.check_launch_registers(_report("combine_kernel", 32) + _report(good, n))
+    for n in (32, 64, 73, 80):
+        with pytest.raises(RuntimeError, match=f"{n} registers"):
+            build.check_launch_registers(_report(good, 72) + _report(good, n))
+    with pytest.raises(RuntimeError, match="no report"):
+        build.check_launch_registers(_report("combine_kernel", 72))
