@@ -133,6 +133,7 @@ struct Shared {
   uint64_t s_full[2], p_full[2];
   uint64_t q_full, m_full, m_free;
   uint64_t drained;  // the products in flight when a wait ran out
+  uint32_t tokens[2];  // of all usable rows: sums of the low 16 bits and of the others
   uint64_t x_full[2][4];  // [slot][quarter of the rows]: the two halves' maxima
   uint64_t d_full[2], d_empty[2];
   uint64_t ring_full[kRing], ring_empty[kRing];
@@ -236,12 +237,21 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
   return v;
 }
 
+// Whether the usable rows have more tokens than there are (see scan_rows).
+__device__ __forceinline__ bool overlapping(const ChunkArgs& a, const Shared* sh) {
+  return (static_cast<unsigned long long>(sh->tokens[1]) << 16) + sh->tokens[0] >
+         static_cast<unsigned long long>(a.num_tokens);
+}
+
 // Inclusive prefix sums of the rows' costs into pref[0 .. batch) (all warps;
 // ends with a CTA barrier); the errors of unusable rows are flagged once.
+// Offsets that do not ascend can leave rows that overlap, with more tokens in
+// all than there are and more work than 32 bits count: then there is none.
 template <class C>
 __device__ __forceinline__ void scan_rows(const ChunkArgs& a, int* pref, Shared* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool reports = blockIdx.x == 0;
+  uint32_t tokens_lo = 0, tokens_hi = 0;
   if (a.max_units > 8) {  // long chunks: a warp per row
     for (int b = warp; b < a.batch; b += kThreads / 32) {
       const RowInfo r = row_info(a, b);
@@ -250,6 +260,8 @@ __device__ __forceinline__ void scan_rows(const ChunkArgs& a, int* pref, Shared*
       for (int m = lane; m < mt; m += 32) c += unit_cost<C>(a, r.n, r.len, m);
       c = warp_sum(c);
       if (lane == 0) {
+        tokens_lo += r.n & 0xffff;
+        tokens_hi += r.n >> 16;
         pref[b] = c;
         if (reports && r.bad) flag_error(a.err, KVQ_DEVERR_BAD_POS);
         if (reports && r.longer) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);
@@ -261,12 +273,20 @@ __device__ __forceinline__ void scan_rows(const ChunkArgs& a, int* pref, Shared*
       const int mt = (r.n * a.gq + C::UNIT - 1) / C::UNIT;
       int c = 0;
       for (int m = 0; m < mt; ++m) c += unit_cost<C>(a, r.n, r.len, m);
+      tokens_lo += r.n & 0xffff;
+      tokens_hi += r.n >> 16;
       pref[b] = c;
       if (reports && r.bad) flag_error(a.err, KVQ_DEVERR_BAD_POS);
       if (reports && r.longer) flag_error(a.err, KVQ_DEVERR_SEQ_LEN);
     }
   }
   __syncthreads();
+  tokens_lo = __reduce_add_sync(0xffffffffu, tokens_lo);
+  tokens_hi = __reduce_add_sync(0xffffffffu, tokens_hi);
+  if (lane == 0 && (tokens_lo | tokens_hi) != 0) {
+    atomicAdd(&sh->tokens[0], tokens_lo);
+    atomicAdd(&sh->tokens[1], tokens_hi);
+  }
   if (warp == 0) {
     int before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
@@ -278,6 +298,7 @@ __device__ __forceinline__ void scan_rows(const ChunkArgs& a, int* pref, Shared*
     if (lane == 0) sh->total = before;
   }
   __syncthreads();
+  if (reports && threadIdx.x == 0 && overlapping(a, sh)) flag_error(a.err, KVQ_DEVERR_BAD_POS);
 }
 
 // A loop count that the compiler does not see through: loops that are to stay
@@ -536,7 +557,7 @@ template <class C>
 __device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const int* pref,
                                           const Waiter& wait) {
   const int lane = threadIdx.x & 31;
-  const int Wu = sh->total;
+  const int Wu = overlapping(a, sh) ? 0 : sh->total;
   const long long W = static_cast<long long>(Wu) * a.c.kv_heads;
   long long share = (W + gridDim.x - 1) / gridDim.x;
   if (share < a.min_share) share = a.min_share;
@@ -1357,6 +1378,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
       mbar_init(&sh->ring_empty[i], 2 * C::PARTS);
     }
     sh->abort = 0;
+    sh->tokens[0] = sh->tokens[1] = 0;
     fence_barrier_init();
   }
   if (warp == kWarpMma) {

@@ -433,3 +433,25 @@ def test_chunk_wait_that_runs_out(drop_stage, lens, n_new, dtype, D, bits):
     for t, before in zip((cache.k_codes, cache.v_codes, cache.k_params), bytes_before):
         assert torch.equal(t, before)
     assert torch.equal(run(), ref) and kvq.kvq_last_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [40, 1500])
+def test_rows_that_overlap(n, dtype):
+    """Offsets that go back leave rows that name the same tokens: as much work as
+    there are rows, whatever num_tokens says.  Nothing is attended then."""
+    B, lens = 7, [1600] * 7
+    cache, users = make_cache(B, 2, 64, 2048, 4, 2, 64, P=64, spare=1, want=lens)
+    kd, vd, cu_kv = fill(cache, users, lens, 1)
+    q = tokens(n, 4, 64, dtype, 2)
+    out = torch.full_like(q, 7.0)
+    kvq.kvq_chunk_attention(cache, q, i32([0, n, 0, n, 0, n, 0, n]), i32(lens), n, 1600, out=out)
+    assert kvq.kvq_device_error_flags() == kvq.KVQ_DEVERR_BAD_POS
+    assert (out == 7.0).all()
+    # one step back, and no overlap: the usable row is served
+    cu = [n, n, n, 0, n, n, n, n]
+    kvq.kvq_chunk_attention(cache, q, i32(cu), i32(lens), n, 1600, out=out)
+    assert kvq.kvq_device_error_flags() == kvq.KVQ_DEVERR_BAD_POS
+    want, tol = attention_reference(q, kd, vd, cu_kv, [0, 0, 0, 0, n, n, n, n], lens, True, 0.0,
+                                    q.dtype)
+    assert_close(out, want, tol)
