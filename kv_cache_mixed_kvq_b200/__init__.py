@@ -242,7 +242,8 @@ class KVCache:
     def _kept_desc(self) -> KvqCacheDesc:
         """The descriptor that the calls share; built and checked again when a
         field, or a buffer's address or layout, has changed since the last one."""
-        k, v, kp, vp, bt = self._buffers()
+        k, v, kp, vp, bt = (self.k_codes, self.v_codes, self.k_params, self.v_params,
+                            self.block_table)
         at = (k.data_ptr(), v.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.is_contiguous(),
               v.is_contiguous(), kp.is_contiguous(), vp.is_contiguous(),
               bt is not None and (bt.data_ptr(), bt.is_contiguous()))
@@ -388,17 +389,19 @@ def _int32(t: torch.Tensor, numel: int, name: str, device: torch.device) -> int:
 def _tokens(t: torch.Tensor, heads: Optional[int], D: int, name: str, device: torch.device):
     """(data pointer, elements from token to token) of packed tokens [T][heads][D];
     a slice along the heads of a larger packed tensor is accepted."""
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [tokens][{heads or 'heads'}][{D}]")
     if t.dtype not in _DTYPE:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
     if t.device != device:
         raise ValueError(f"{name} must be on the cache's device")
-    T, H, _ = t.shape
+    T, H, _ = shape
     if T == 0:
         return None, H * D
-    stride = t.stride(0) if T > 1 else H * D
-    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and H > 1) or stride < H * D or \
+    strides = t.stride()
+    stride = strides[0] if T > 1 else H * D
+    if (strides[2] != 1 and D > 1) or (strides[1] != D and H > 1) or stride < H * D or \
             stride * t.element_size() % 16:
         raise ValueError(f"{name}: the heads of a token must be contiguous and tokens "
                          "a multiple of 16 bytes apart")
@@ -441,12 +444,13 @@ def kvq_plan_append(cache: KVCache, old_lens: torch.Tensor, new_lens: torch.Tens
     lib = library()
     E = lib.kvq_slot_map_entries(B, num_tokens)
     # (one allocation: three took half of the call's host time)
-    slot_map, lens, cu = _empty(4 * E + 2 * B + 1, torch.int32, device,
-                                stream).split_with_sizes((4 * E, B, B + 1))
+    results = _empty(4 * E + 2 * B + 1, torch.int32, device, stream)
+    at = results.data_ptr()
+    slot_map, lens, cu = results.split_with_sizes((4 * E, B, B + 1))
     slot_map = slot_map.view(E, 4)
     d = cache._kept_desc()
-    st = lib.kvq_plan_append(ctypes.byref(d), old, new, num_tokens, users, lens.data_ptr(),
-                             cu.data_ptr(), slot_map.data_ptr() if E else None, E,
+    st = lib.kvq_plan_append(ctypes.byref(d), old, new, num_tokens, users, at + 16 * E,
+                             at + 16 * E + 4 * B, at if E else None, E,
                              _stream_ptr(stream))
     _check(st, "kvq_plan_append")
     if stream is not None:
@@ -492,10 +496,12 @@ def kvq_dequantize_ragged(cache: KVCache, slot_map: torch.Tensor, num_tokens: in
             raise ValueError("dtype must be float32, bfloat16 or float16")
         k_out = _empty(shape, dtype, device, stream)
         v_out = _empty(shape, dtype, device, stream)
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if tuple(t.shape) != shape or t.dtype not in _DTYPE or t.dtype != k_out.dtype or \
-                t.device != device:
-            raise ValueError(f"{name} must be {list(shape)}, on the cache's device, of one dtype")
+    else:
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if tuple(t.shape) != shape or t.dtype not in _DTYPE or t.dtype != k_out.dtype or \
+                    t.device != device:
+                raise ValueError(f"{name} must be {list(shape)}, on the cache's device, of one "
+                                 "dtype")
     sp = _slots(slot_map, device)
     d = cache._kept_desc()
     st = library().kvq_dequantize_ragged(ctypes.byref(d), sp, slot_map.shape[0],
