@@ -22,9 +22,11 @@ __global__ void __launch_bounds__(128) combine_kernel(const ChunkArgs a, int gri
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  const int* hd = a.ws_head + (blockIdx.x * 2 + 1) * 8;
-  if (hd[0] == 0 || hd[5] != 0) return;
-  const int start = hd[1], h = hd[2], row0 = hd[3], rows = hd[4], n = hd[6], len = hd[7];
+  // the header in two loads, both under way before either is looked at
+  const int4* hd = reinterpret_cast<const int4*>(a.ws_head) + (blockIdx.x * 2 + 1) * 2;
+  const int4 h0 = hd[0], h1 = hd[1];
+  if (h0.x == 0 || h1.y != 0) return;
+  const int start = h0.y, h = h0.z, row0 = h0.w, rows = h1.x, n = h1.z, len = h1.w;
   for (int i = warp; i < kCombineRows; i += 4) {
     const int r = blockIdx.y * kCombineRows + i;
     if (r >= rows) return;
