@@ -26,17 +26,19 @@ __global__ void __launch_bounds__(128) combine_kernel(const ChunkArgs a, int gri
   const int4* hd = reinterpret_cast<const int4*>(a.ws_head) + (blockIdx.x * 2 + 1) * 2;
   const int4 h0 = hd[0], h1 = hd[1];
   if (h0.x == 0 || h1.y != 0) return;
-  const int start = h0.y, h = h0.z, row0 = h0.w, rows = h1.x, n = h1.z, len = h1.w;
+  const int start = h0.y, h = h0.z, row0 = h0.w, rows = h1.x;
   for (int i = warp; i < kCombineRows; i += 4) {
     const int r = blockIdx.y * kCombineRows + i;
     if (r >= rows) return;
     float o[N], m = -INFINITY, l = 0.0f;
+    bool nothing = false;  // the row sees no position: its output is 0
 #pragma unroll
     for (int k = 0; k < N; ++k) o[k] = 0.0f;
     int place = blockIdx.x * 2 + 1;
     for (int c = blockIdx.x; c < grid; ++c, place = 2 * c) {
       const size_t prow = static_cast<size_t>(place) * a.part_rows + r;
       const float2 ml = a.ws_ml[prow];
+      nothing = ml.y < 0.0f;
       const float mm = fmaxf(m, ml.x), base = mm == -INFINITY ? 0.0f : mm;
       const float f = exp2_approx(m - base), g = exp2_approx(ml.x - base);
       l = l * f + ml.y * g;
@@ -47,7 +49,6 @@ __global__ void __launch_bounds__(128) combine_kernel(const ChunkArgs a, int gri
       if (a.ws_head[place * 8 + 5] != 0) break;
     }
     const int br = row0 + r;
-    const bool nothing = chunk::limit_of(a, n, len, br) <= 0;  // no position is seen: 0
     const float inv = 1.0f / l;
     const size_t orow =
         (static_cast<size_t>(start + br / a.gq) * a.q_heads + h * a.gq + br % a.gq) * D + lane * N;

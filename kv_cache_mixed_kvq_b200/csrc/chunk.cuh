@@ -621,7 +621,6 @@ __device__ __forceinline__ bool list_role(const ChunkArgs& a, Shared* sh, const 
           if (!(p.begin && p.end)) {
             int* hd = a.ws_head + (blockIdx.x * 2 + p.begin) * 8;
             hd[0] = 1; hd[1] = r.start; hd[2] = h; hd[3] = u.row0; hd[4] = u.rows; hd[5] = p.end;
-            hd[6] = r.n; hd[7] = r.len;
             headers |= 1u << p.begin;
           }
         }
@@ -1274,7 +1273,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkArgs& a, Shared* sh, uin
       // the row's place in the output, or among the partial results
       const size_t prow = static_cast<size_t>(blockIdx.x * 2 + part) * a.part_rows + ur;
       if (!whole && valid && half == 0)
-        a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, l);
+        a.ws_ml[prow] = make_float2(m == -INFINITY ? m : m * c, limit <= 0 ? -1.0f : l);
       const int type = whole ? a.out_dtype : static_cast<int>(KVQ_F32);
       const size_t row = whole ? (static_cast<size_t>(token) * a.q_heads + head) * D : prow * D;
       const int es = type == KVQ_F32 ? 4 : 2;

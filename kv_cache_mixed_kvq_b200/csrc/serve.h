@@ -92,10 +92,8 @@ struct ChunkArgs {
   // partial results of units cut by a share's border, two places per CTA
   // (0: a piece that continues a unit, 1: one that begins it)
   int part_rows;  // rows of a place
-  // [grid][2][8]: valid, first token, kv head, first row, rows, last piece, the
-  // batch row's tokens and length
-  int* ws_head;
-  float2* ws_ml;  // [grid][2][part_rows]: (reference exponent, sum)
+  int* ws_head;   // [grid][2][8]: valid, first token, kv head, first row, rows, last piece
+  float2* ws_ml;  // [grid][2][part_rows]: (reference exponent, sum; -1: the row sees nothing)
   float* ws_o;    // [grid][2][part_rows][D]
   // Failure-detection test knob (kvq_debug_inject_wait_timeout): when
   // fault_stage is 0 or 1, that block of the first CTA's ring expects one
