@@ -499,7 +499,9 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  *   t in [0, seq_lens[b] - n_b + i]  (causal != 0), or [0, seq_lens[b]).
  * A query that sees no position yields o = 0.  NaN and infinities of a query,
  * or of the parameters of a position that it sees, make its output NaN (or
- * infinite) as the formula does; they are not flagged.
+ * infinite) as the formula does; they are not flagged.  (The cache's inputs are
+ * finite, see above.  Should a value's parameters not be, then 0 * NaN also
+ * reaches the earlier queries of a causal chunk that share its tile.)
  *
  *   q           : device, token t of query head hq at t * q_stride + hq * D,
  *                 q_dtype, 16-byte aligned; q_stride >= Hq * D, a multiple of

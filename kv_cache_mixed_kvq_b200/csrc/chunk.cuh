@@ -35,8 +35,8 @@
 //   warp 24     issues the MMAs
 //   warp 25     walks the work list and publishes each piece of work
 //   warps 26-27 copy packed codes and parameters, 32 positions at a time, into
-//               the ring (cp.async: four bulk copies a block, each set up in
-//               uniform registers, took 900 cycles of the one warp)
+//               the ring (cp.async: four bulk copies a block, issued by one
+//               lane, took 900 cycles)
 // In a wide unit (more than 128 rows) the slots are its two halves and share
 // each K and V tile; in a narrow one they take alternate tiles of the same
 // rows and are merged at the end, so that one slot's softmax runs while the

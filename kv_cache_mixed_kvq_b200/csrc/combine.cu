@@ -9,6 +9,7 @@
 // partials of a row are those of the CTAs that covered its unit.
 #include "common.cuh"
 #include "internal.h"
+#include "token_rows.cuh"
 
 namespace kvq {
 namespace {

@@ -76,15 +76,6 @@ __device__ __forceinline__ void flag_error(uint32_t* err, uint32_t bits) {
   if (err) atomicOr(err, bits);
 }
 
-// ------------------------------------------------------- single-token rows
-// Row of q and out that is batch row b's one token, from the offsets of a
-// ragged step; -1: it has none, -2: its offsets are not usable.
-__device__ __forceinline__ int single_token_row(const int32_t* cu, int num_tokens, int b) {
-  const int start = __ldg(cu + b), end = __ldg(cu + b + 1);
-  if (start < 0 || end < start || end > num_tokens || end - start > 1) return -2;
-  return end > start ? start : -1;
-}
-
 // ------------------------------------------------ balanced decode schedule
 // off[r] = units * sum_{r' < r} ceil(len_r' / T) for r = 0 .. kStreamRows,
 // with each length clamped to [0, lim] (rows past `batch` count nothing);

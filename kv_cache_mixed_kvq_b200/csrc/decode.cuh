@@ -48,6 +48,7 @@
 #include "append_rows.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "token_rows.cuh"
 
 namespace kvq {
 
@@ -265,9 +266,10 @@ __device__ __forceinline__ size_t token_row(const DecodeArgs& a, int b) {
 }
 
 // Bulk copy of span s's query rows (heads head0 .. head0 + nh - 1 of row
-// `row` of q, [head][D] in the query type) into a query buffer; thread 0 only.  The
-// rows are contiguous, start on a multiple of 128 bytes from the query base
-// (16-byte aligned, as the API requires) and are whole 16-byte units.
+// `row` of q, [head][D] in the query type) into a query buffer; thread 0
+// only.  The rows are contiguous, start on a multiple of 128 bytes from the
+// query base (16-byte aligned, as the API requires) and are whole 16-byte
+// units.
 template <class C>
 __device__ __forceinline__ void issue_q_rows(const DecodeArgs& a, const Span& s, size_t row,
                                              uint8_t* dst, uint64_t* bar) {

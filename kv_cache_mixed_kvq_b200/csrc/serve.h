@@ -63,8 +63,16 @@ constexpr int tile_tokens(int pieces, int head_dim, int bits_kv) {
   return pieces == 1 && !(head_dim == 128 && bits_kv == 16) ? 128 : 64;
 }
 // Steps that a unit's queries and output are worth in the division of work (20
-// thousand cycles on B200, a step about 5; ragged prefill 516 us with 2, 488 with 3
-// and 5, verification 100, 98 and 105).
+// thousand cycles on B200 for bf16 and head_dim 128, a step about 5).  One value
+// for all instances: measured with 1, 2, 3, 5 and 8, us on B200,
+//   prefill of 4 rows of 2000-4000 tokens  bf16 569 534 510 489 526, head_dim 64
+//     455 424 407 430 466, K8V8 726 704 676 637 641, f16 862 841 814 799 818,
+//     f32 1470 1405 1425 1483 1575, head_dim 64 1146 1140 1158 1193 1248;
+//   6 rows of 100-700 tokens  bf16 121 105 97 97 103, f16 150 131 120 116 125,
+//     f32 252 225 226 237 244;
+//   16 rows of 4 tokens  bf16 86 86 89 93 101, f16 135 136 140 144 152,
+//     f32 158 155 158 164 172.
+// (3 is within 6 % of the best of each.)
 constexpr int kUnitCost = 3;
 // Batch rows one call takes (their prefix sums lie in the tiles' memory).
 constexpr int kChunkRows = 16384;
