@@ -55,14 +55,14 @@
 // cycles; of these the tensor pipe is busy for 2000 (its products alone, as
 // issued here, take 2800: 102 cycles per 128 x 128 x 16 product with both
 // operands in shared memory, 73 with the weights in tensor memory), the
-// exponentials 2000, and 12,200 warp instructions are issued (61 % of issue
+// exponentials 2000, and 12,300 warp instructions are issued (63 % of issue
 // slots).  Between two products of a slot lies its softmax, whose chain
 // (scores, maxima, exchange, weights) is what the other slot's products
 // hide.  Measured on B200: 2048 queries of 32 heads (8 kv heads, K4V2) at
 // position 24576, 0.97-1.02 ms = 0.84-0.88 PFLOP/s (half of the measured bf16
-// peak of 1.66); ragged prefill of 4 x 2000-4000 tokens, 0.485 ms = 0.60
+// peak of 1.66); ragged prefill of 4 x 2000-4000 tokens, 0.488 ms = 0.60
 // PFLOP/s.  Narrow units are bound by the same chain with few valid rows: 16
-// rows x 4 tokens x 4256 positions on average, 87 us (0.73 TB/s of cache bytes).
+// rows x 4 tokens x 4256 positions on average, 88 us (0.72 TB/s of cache bytes).
 // What was measured and not kept, in us for these three cases where the kept
 // form of its time took 1010, 558 and 107: tiles of 64 positions with the next
 // tile's scores ahead of the softmax (1124, 791, 135), weights held in registers
