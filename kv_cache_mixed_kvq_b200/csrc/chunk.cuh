@@ -182,12 +182,14 @@ struct RowInfo {
 
 __device__ __forceinline__ RowInfo row_info(const ChunkArgs& a, int b) {
   RowInfo r;
-  r.start = __ldg(a.cu + b);
-  const int end = __ldg(a.cu + b + 1);
+  // (coherent loads, as everywhere that the planner may just have written: the
+  // launch may have begun before it ended)
+  r.start = a.cu[b];
+  const int end = a.cu[b + 1];
   r.bad = r.start < 0 || end < r.start || end - r.start > a.max_q_len || end > a.num_tokens;
   r.n = r.bad ? 0 : end - r.start;
   const int lim = min(a.max_seq_len, a.capacity);
-  const int len = __ldg(a.seq_lens + b);
+  const int len = a.seq_lens[b];
   r.longer = len > lim;
   r.len = max(0, min(len, lim));
   return r;
@@ -695,7 +697,7 @@ __device__ __forceinline__ bool copy_role(const ChunkArgs& a, Shared* sh, uint8_
         const int q = p + lane * kBlock;
         page = b;
         if (a.table != nullptr && q < last) {
-          page = __ldg(a.table + static_cast<size_t>(b) * a.pages_per_seq + (q >> a.page_shift));
+          page = a.table[static_cast<size_t>(b) * a.pages_per_seq + (q >> a.page_shift)];
           if (page < 0 || page >= a.c.blocks) {
             flag_error(a.err, KVQ_DEVERR_BAD_PAGE);
             page = -1;
@@ -938,9 +940,8 @@ __device__ __forceinline__ void load_queries(const ChunkArgs& a, size_t off, boo
       const size_t at = __shfl_sync(0xffffffffu, off, row) + 8 * u;
       raw[i] = make_uint4(0, 0, 0, 0);
       if ((kinds >> row) & 1)
-        raw[i] = f32 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at) +
-                             (i & 1))
-                     : __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+        raw[i] = f32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at)[i & 1]
+                     : *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
     }
 #pragma unroll 1
     for (int t = t0; t < t0 + turns; ++t) {

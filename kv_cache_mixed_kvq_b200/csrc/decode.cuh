@@ -261,7 +261,7 @@ struct Span {
 // append and the balanced schedule have no offsets.
 template <bool FUSED>
 __device__ __forceinline__ size_t token_row(const DecodeArgs& a, int b) {
-  if (!FUSED && __builtin_expect(a.cu != nullptr, 0)) b = __ldg(a.cu + b);
+  if (!FUSED && __builtin_expect(a.cu != nullptr, 0)) b = a.cu[b];
   return static_cast<size_t>(b);
 }
 

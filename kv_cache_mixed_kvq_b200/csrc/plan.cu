@@ -90,7 +90,7 @@ struct Row {
 };
 
 __device__ __forceinline__ Row load_row(const PlanArgs& a, int b) {
-  Row r{__ldg(a.old_lens + b), __ldg(a.new_lens + b), true};
+  Row r{a.old_lens[b], a.new_lens[b], true};  // (the planner's results of the call before, perhaps)
   if (r.o < 0 || r.n < 0 || r.o > a.capacity || r.n > a.capacity) {
     r.ok = false;
     r.n = r.o;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const Row r = load_row(a, b);
       bool refused = !r.ok;
       if (refused && rank == 0)
-        flag_error(a.err, r.o < 0 || __ldg(a.new_lens + b) < 0 ? KVQ_DEVERR_BAD_POS
+        flag_error(a.err, r.o < 0 || a.new_lens[b] < 0 ? KVQ_DEVERR_BAD_POS
                                                                : KVQ_DEVERR_SEQ_LEN);
       if (r.n > r.o) {
         n_new = r.n - r.o;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         if (r < taken) {
           const int b = first_above(s_upto, a.batch, r);
           const int first = b > 0 ? s_upto[b - 1] : 0;
-          const int have = (__ldg(a.old_lens + b) + P1) >> a.page_shift;
+          const int have = (a.old_lens[b] + P1) >> a.page_shift;
           a.table[static_cast<size_t>(b) * a.pages_per_seq + have + (r - first)] = i + x;
           a.users[i + x] = 1;
         }

@@ -27,6 +27,8 @@
 // K4V2, on B200: append 16.3 us (2.5 TB/s in and out, 77 % of issue slots),
 // read-back 11.1 us; with one unit a thread 39 and 24 us, since the group's
 // exchanges and quotients are per thread.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "serve.h"
@@ -37,7 +39,7 @@ namespace {
 // Entry e of the map if it names places inside the cache and the packed
 // tokens; count 0 (and an error flag) otherwise.
 __device__ __forceinline__ int4 load_entry(const RaggedArgs& a, int e) {
-  int4 m = __ldg(a.map + e);
+  int4 m = a.map[e];  // (coherent: the planner may be the kernel before)
   if (m.w == 0) return m;
   uint32_t bad = 0;
   if (m.x < 0 || m.x >= a.c.blocks) bad |= KVQ_DEVERR_BAD_PAGE;
@@ -110,11 +112,31 @@ __device__ __forceinline__ uint32_t v_half_offset(int D, uint32_t b, uint32_t k,
   return ((n >> ps) << (ps + 5)) + (((k & 7) >> 1) << ps) + (n & ((1u << ps) - 1));
 }
 
-// 16 elements widened to binary32.
+// 16 elements widened to binary32, by coherent loads (the read-back may be the
+// kernel before).
 template <typename T>
 __device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
-  Load8<T>::run(p, *reinterpret_cast<float(*)[8]>(x));
-  Load8<T>::run(p + 8, *reinterpret_cast<float(*)[8]>(x + 8));
+  constexpr int N = static_cast<int>(sizeof(T));  // 16-byte loads
+  uint4 u[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (std::is_same<T, float>::value) {
+        x[4 * i + k] = __uint_as_float(w[k]);
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+        x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      } else {
+        const float2 f = unpack_half2(w[k]);
+        x[8 * i + 2 * k] = f.x;
+        x[8 * i + 2 * k + 1] = f.y;
+      }
+    }
+  }
 }
 
 template <int D, typename TIn, bool ROT>

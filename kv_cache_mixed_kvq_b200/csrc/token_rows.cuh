@@ -7,9 +7,10 @@
 namespace kvq {
 
 // Row of q and out that is batch row b's one token, from the offsets of a
-// ragged step; -1: it has none, -2: its offsets are not usable.
+// ragged step (which the kernel before may have written: coherent loads); -1:
+// it has none, -2: its offsets are not usable.
 __device__ __forceinline__ int single_token_row(const int32_t* cu, int num_tokens, int b) {
-  const int start = __ldg(cu + b), end = __ldg(cu + b + 1);
+  const int start = cu[b], end = cu[b + 1];
   if (start < 0 || end < start || end > num_tokens || end - start > 1) return -2;
   return end > start ? start : -1;
 }

@@ -455,3 +455,95 @@ def test_rows_that_overlap(n, dtype):
     want, tol = attention_reference(q, kd, vd, cu_kv, [0, 0, 0, 0, n, n, n, n], lens, True, 0.0,
                                     q.dtype)
     assert_close(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tile_attention_right_after_the_plan(dtype):
+    """Offsets and lengths that the kernel before writes, by the tile kernel."""
+    B, P, cap, pages = 64, 32, 1024, 1 << 20
+    planned = _plan_only(B, cap, P, pages, torch.full((B, cap // P), -1, dtype=torch.int32,
+                                                      device="cuda"))
+    users = torch.ones(pages, dtype=torch.int32, device="cuda")
+    users[-3000:] = 0
+    cache, _ = make_cache(B, 1, 64, cap, 4, 2, 64)
+    fill(cache, None, [cap] * B, 1)
+    q = tokens(3 * B, 4, 64, dtype, 3)
+    steps = []
+    for i in range(12):
+        old = [32 * ((7 * b + 5 * i) % 31) for b in range(B)]
+        steps.append((i32(old), i32([n + 1 + (b + i) % 3 for b, n in enumerate(old)])))
+    want = []
+    for old, new in steps:
+        cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+        cu[1:] = (new - old).cumsum(0)
+        want.append((int(cu[-1]), kvq.kvq_chunk_attention(cache, q, cu, new, 3, cap)))
+    torch.cuda.synchronize()
+    got = []
+    for old, new in steps:
+        lens, cu, _ = kvq.kvq_plan_append(planned, old, new, 3 * B, users)
+        got.append(kvq.kvq_chunk_attention(cache, q, cu, lens, 3, cap))
+    torch.cuda.synchronize()
+    assert kvq.kvq_device_error_flags() == 0
+    for x, (n, y) in zip(got, want):
+        assert torch.equal(x[:n], y[:n])
+
+
+def test_append_right_after_the_plan_and_the_read_back():
+    """A prefix moved to another cache: plan, read-back and append in a chain,
+    each reading what the one before writes."""
+    T, H, D = 700, 2, 128
+    a, _ = make_cache(1, H, D, 1024, 8, 8, 32)
+    kd, vd, _ = fill(a, None, [T], 1)
+    moved, _ = make_cache(1, H, D, 1024, 4, 2, 64)
+    slots = kvq.kvq_plan_append(a, i32([0]), i32([T]), T)[2]
+    kvq.kvq_quantize_append_ragged(moved, kd, vd, slots)
+    want = [t.clone() for t in (moved.k_codes, moved.v_codes, moved.k_params, moved.v_params)]
+    old, new = i32([0]), i32([T])
+    ko, vo = torch.zeros_like(kd), torch.zeros_like(vd)
+    for _ in range(8):
+        for t in (moved.k_codes, moved.v_codes, moved.k_params, moved.v_params):
+            t.zero_()
+        ko.zero_(), vo.zero_()
+        slots = kvq.kvq_plan_append(moved, old, new, T)[2]
+        kvq.kvq_dequantize_ragged(a, slots, T, k_out=ko, v_out=vo)
+        kvq.kvq_quantize_append_ragged(moved, ko, vo, slots)
+        for t, w in zip((moved.k_codes, moved.v_codes, moved.k_params, moved.v_params), want):
+            assert torch.equal(t, w)
+    assert kvq.kvq_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("env", [("KVQ_DECODE_KERNEL", "tcgen05"), ("KVQ_SPLIT_TOKENS", "64"),
+                                 ("KVQ_DECODE_SCHEDULE", "balanced")])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_padded_single_tokens_with_the_decode_settings(env, dtype, monkeypatch):
+    """The opt-in kernel and schedule do not look rows up: they are not taken."""
+    monkeypatch.setenv(*env)
+    lens = [100, 3000, 64, 1, 2111, 0]
+    cache, users = make_cache(6, 2, 128, 4096, 4, 2, 64, 0, False, 64, 3, want=lens)
+    kd, vd, cu_kv = fill(cache, users, lens, 1)
+    q, cu = tokens(6, 16, 128, dtype, 9), [0, 1, 2, 2, 3, 4, 4]
+    out = torch.full_like(q, 7.0)
+    kvq.kvq_chunk_attention(cache, q, i32(cu), i32(lens), 1, max(lens), out=out)
+    assert kvq.kvq_device_error_flags() == 0 and (out[4:] == 7.0).all()
+    want, tol = attention_reference(q[:4], kd, vd, cu_kv, cu, lens, True, 0.0, q.dtype)
+    assert_close(out[:4], want, tol)
+
+
+def test_captured_calls_on_the_capture_stream_by_argument():
+    """stream= inside a capture: the results are the graph's memory."""
+    lens = [1500, 40]
+    cache, users = make_cache(2, 2, 128, 2048, 4, 2, 64, P=64, spare=1, want=lens)
+    fill(cache, users, lens, 1)
+    q, cu, at = tokens(40, 4, 128, "bf16", 2), i32([0, 20, 40]), i32(lens)
+    want = kvq.kvq_chunk_attention(cache, q, cu, at, 20, 1500)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = kvq.kvq_chunk_attention(cache, q, cu, at, 20, 1500, stream=s)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert kvq.kvq_device_error_flags() == 0
