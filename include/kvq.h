@@ -523,11 +523,11 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* cache, int32_t num_q_head
  * Lengths above max_seq_len or capacity are clamped and flag
  * KVQ_DEVERR_SEQ_LEN; rows whose offsets are not ascending, pass num_tokens
  * or exceed max_q_len are skipped and flag KVQ_DEVERR_BAD_POS (all rows, if
- * those that are left overlap and have more than num_tokens together).  Block-table
- * entries outside the pool flag KVQ_DEVERR_BAD_PAGE, are not followed, and
- * leave that row's output unspecified.  batch <= 16384, and lengths,
- * num_tokens * Hq and the (query tile, key tile) pairs of a kv head stay
- * within 2^30 (KVQ_ERR_UNSUPPORTED above).
+ * those that are left overlap and have more than num_tokens together).
+ * Block-table entries outside the pool flag KVQ_DEVERR_BAD_PAGE, are not
+ * followed, and leave that row's output unspecified.  batch <= 16384, and
+ * lengths, num_tokens * Hq and the (query tile, key tile) pairs of a kv head
+ * stay within 2^30 (KVQ_ERR_UNSUPPORTED above).
  *
  * Kernel launches: one, and a second one that joins partial results when rows
  * are long enough to be divided; 16-bit queries of max_q_len = 1 and
